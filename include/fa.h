@@ -269,6 +269,95 @@ FA_API int fa_decode_int4_paged(const void* q, const uint8_t* k_pages, const uin
                                 int num_splits, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
+/*
+ * Writing a quantised KV cache (source: "Flash Attention on Ascend: three techniques", section 3,
+ * KV compression).  One row is one token of one KV head; its D bf16 values x become
+ *   scale = max|x| / m rounded to fp32,  code = clamp(rint(x / scale), -m, m),  m = 127 (INT8) or
+ * 7 (INT4), the quotient rounded to fp32 and rint to even on ties; a row of zeros gets scale 0
+ * and codes 0.  A row that holds an infinity or a NaN gets scale NaN and codes 0: whatever reads
+ * it is NaN.  These are the caches fa_decode_int8 / fa_decode_int4 read (INT4 packed as there).
+ *   k, v             bf16 [B, Skv, Hkv, D]
+ *   k_codes, v_codes int8 [B, Skv, Hkv, D], or uint8 [B, Skv, Hkv, D/2]   written
+ *   k_scale, v_scale fp32 [B, Hkv, Skv]                                   written
+ * D must be 64 or 128; B * Skv < 2^31.  Returns FA_OK or an fa_status error code; nothing is
+ * launched on error.
+ */
+FA_API int fa_kv_quantize_int8(const void* k, const void* v, int8_t* k_codes, int8_t* v_codes,
+                               float* k_scale, float* v_scale, int B, int Skv, int Hkv, int D,
+                               void* stream);
+FA_API int fa_kv_quantize_int4(const void* k, const void* v, uint8_t* k_codes, uint8_t* v_codes,
+                               float* k_scale, float* v_scale, int B, int Skv, int Hkv, int D,
+                               void* stream);
+
+/*
+ * Reading such a cache back: k, v bf16 [B, Skv, Hkv, D] = code * scale, the product rounded to
+ * fp32 and then to bf16.  Arguments as for fa_kv_quantize_int8 / fa_kv_quantize_int4.
+ */
+FA_API int fa_kv_dequantize_int8(const int8_t* k_codes, const int8_t* v_codes,
+                                 const float* k_scale, const float* v_scale, void* k, void* v,
+                                 int B, int Skv, int Hkv, int D, void* stream);
+FA_API int fa_kv_dequantize_int4(const uint8_t* k_codes, const uint8_t* v_codes,
+                                 const float* k_scale, const float* v_scale, void* k, void* v,
+                                 int B, int Skv, int Hkv, int D, void* stream);
+
+/*
+ * Appending new tokens to a paged cache (the layout fa_decode_int8_paged reads), quantised as by
+ * fa_kv_quantize_int8: the write of a decode step (one token per sequence) or of a batch of
+ * prompts of different lengths.
+ *   k, v       bf16, token row i ([Hkv, D], contiguous) at k + i * k_stride and v + i * v_stride
+ *              elements, so that K and V may be slices of one projection's output; the strides are
+ *              multiples of 8 and at least Hkv * D.
+ *   cu_tokens  int32 [B + 1] (device) or NULL.  Rows cu_tokens[b] .. cu_tokens[b + 1] - 1 are the
+ *              new tokens of sequence b; it starts at 0 and ascends (a sequence may have none).
+ *              Rows from cu_tokens[B] to num_tokens - 1 belong to no sequence and are not read.
+ *              NULL: num_tokens / B tokens of each sequence.
+ *   positions  int32 [B] (device) or NULL (all 0): position of each sequence's first new token,
+ *              i.e. its length before the call.
+ *   block_table  int32 [B, max_pages_per_seq] (device): position j of sequence b is row
+ *              j % page_size of page block_table[b][j / page_size].
+ *   k_pages, v_pages, k_scale_pages, v_scale_pages, page_size, num_pages  as for
+ *              fa_decode_int8_paged / fa_decode_int4_paged; only the new tokens' rows are written.
+ * num_tokens = 0 does nothing (k and v may then be NULL).  Two tokens of one call must not share
+ * a cache row (their codes and scales would mix).  A position outside the table, a page
+ * id outside the pool or offsets that do not ascend from 0 to at most num_tokens are recorded on
+ * the device (FA_ERR_DEVICE_INDEX from fa_device_status) and the rows they concern are not written;
+ * no access leaves the buffers.
+ */
+FA_API int fa_kv_append_int8_paged(const void* k, const void* v, int64_t k_stride,
+                                   int64_t v_stride, int8_t* k_pages, int8_t* v_pages,
+                                   float* k_scale_pages, float* v_scale_pages,
+                                   const int32_t* block_table, const int32_t* positions,
+                                   const int32_t* cu_tokens, int num_tokens, int B, int Hkv,
+                                   int page_size, int max_pages_per_seq, int num_pages, int D,
+                                   void* stream);
+FA_API int fa_kv_append_int4_paged(const void* k, const void* v, int64_t k_stride,
+                                   int64_t v_stride, uint8_t* k_pages, uint8_t* v_pages,
+                                   float* k_scale_pages, float* v_scale_pages,
+                                   const int32_t* block_table, const int32_t* positions,
+                                   const int32_t* cu_tokens, int num_tokens, int B, int Hkv,
+                                   int page_size, int max_pages_per_seq, int num_pages, int D,
+                                   void* stream);
+
+/*
+ * Reading tokens of a paged cache back as bf16, e.g. a context that fa_fwd attends to while the
+ * next chunk of a prompt is computed: the mirror of fa_kv_append_int8_paged.
+ *   k, v   bf16 [num_tokens, Hkv, D]: row cu_tokens[b] + i is position positions[b] + i of
+ *          sequence b.  Rows behind the last sequence, and rows whose position or page id is out
+ *          of range (recorded as above), are left as they were.
+ */
+FA_API int fa_kv_gather_int8_paged(const int8_t* k_pages, const int8_t* v_pages,
+                                   const float* k_scale_pages, const float* v_scale_pages,
+                                   const int32_t* block_table, const int32_t* positions,
+                                   const int32_t* cu_tokens, void* k, void* v, int num_tokens,
+                                   int B, int Hkv, int page_size, int max_pages_per_seq,
+                                   int num_pages, int D, void* stream);
+FA_API int fa_kv_gather_int4_paged(const uint8_t* k_pages, const uint8_t* v_pages,
+                                   const float* k_scale_pages, const float* v_scale_pages,
+                                   const int32_t* block_table, const int32_t* positions,
+                                   const int32_t* cu_tokens, void* k, void* v, int num_tokens,
+                                   int B, int Hkv, int page_size, int max_pages_per_seq,
+                                   int num_pages, int D, void* stream);
+
 /* Static, human-readable name of a status code.  Never NULL. */
 FA_API const char* fa_status_string(int status);
 

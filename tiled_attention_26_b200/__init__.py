@@ -8,12 +8,16 @@ every call raises; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
 
 __all__ = ["FaError", "lib", "fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_decode_int8", "fa_decode_int8_paged",
            "fa_decode_int4", "fa_decode_int4_paged", "fa_decode_int8_workspace_bytes",
+           "fa_kv_quantize_int8", "fa_kv_quantize_int4", "fa_kv_dequantize_int8", "fa_kv_dequantize_int4",
+           "fa_kv_append_int8_paged", "fa_kv_append_int4_paged", "fa_kv_gather_int8_paged",
+           "fa_kv_gather_int4_paged",
            "fa_status_string", "fa_device_status", "fa_selftest_bounded_wait", "LIB_PATH",
            "STATUS"]
 
@@ -71,6 +75,16 @@ def lib() -> ctypes.CDLL:
         L.fa_decode_int4.restype = _I
         L.fa_decode_int4_paged.argtypes = [_P] * 9 + [_I] * 7 + [_F, _I, _P, _Z, _P]
         L.fa_decode_int4_paged.restype = _I
+        for bits in (8, 4):
+            f = getattr(L, f"fa_kv_quantize_int{bits}")
+            f.argtypes, f.restype = [_P] * 6 + [_I] * 4 + [_P], _I
+            f = getattr(L, f"fa_kv_dequantize_int{bits}")
+            f.argtypes, f.restype = [_P] * 6 + [_I] * 4 + [_P], _I
+            f = getattr(L, f"fa_kv_append_int{bits}_paged")
+            f.argtypes = [_P, _P, ctypes.c_int64, ctypes.c_int64] + [_P] * 7 + [_I] * 7 + [_P]
+            f.restype = _I
+            f = getattr(L, f"fa_kv_gather_int{bits}_paged")
+            f.argtypes, f.restype = [_P] * 9 + [_I] * 7 + [_P], _I
         L.fa_status_string.argtypes = [_I]
         L.fa_status_string.restype = ctypes.c_char_p
         L.fa_device_status.argtypes = [_P]
@@ -311,6 +325,238 @@ def fa_decode_int4_paged(q, k_pages, v_pages, k_scale_pages, v_scale_pages, bloc
     [num_pages, P, Hkv, D/2] packed as for fa_decode_int4; otherwise as fa_decode_int8_paged."""
     return _decode_paged(4, q, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table,
                          seqlens, num_splits, scale, o, lse, workspace, return_lse, stream)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(dev, stream):
+    """Context in which a call's buffers are allocated and its kernels launched: the tensors'
+    device, and ``stream`` (whose device it must be) where one is given, so that a buffer the call
+    allocates belongs to the stream that uses it."""
+    import torch
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {dev}")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
+        return torch.cuda.stream(stream)
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _code_type(bits, D):
+    """dtype and elements of one row of D codes."""
+    import torch
+    return (torch.int8, D) if bits == 8 else (torch.uint8, D // 2)
+
+
+def _kv_quantize(bits, k, v, k_codes, v_codes, k_scale, v_scale, stream):
+    import torch
+    name = f"fa_kv_quantize_int{bits}"
+    if k.dim() != 4:
+        raise ValueError("k, v must be 4-D [B, S, Hkv, D]")
+    B, S, Hkv, D = k.shape
+    dev = k.device
+    code, row = _code_type(bits, D)
+    _check(k, "k", torch.bfloat16, (B, S, Hkv, D), dev)
+    _check(v, "v", torch.bfloat16, (B, S, Hkv, D), dev)
+    with _on(dev, stream):
+        out = []
+        for t, what in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+            t = torch.empty((B, S, Hkv, row), dtype=code, device=dev) if t is None else t
+            _check(t, what, code, (B, S, Hkv, row), dev)
+            out.append(t)
+        for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            t = torch.empty((B, Hkv, S), dtype=torch.float32, device=dev) if t is None else t
+            _check(t, what, torch.float32, (B, Hkv, S), dev)
+            out.append(t)
+        rc = getattr(lib(), name)(k.data_ptr(), v.data_ptr(), *(t.data_ptr() for t in out), B, S,
+                                  Hkv, D, _stream_ptr(None))
+    if rc != 0:
+        raise FaError(rc, name)
+    return tuple(out)
+
+
+def fa_kv_quantize_int8(k, v, k_codes=None, v_codes=None, k_scale=None, v_scale=None, stream=None):
+    """Quantise whole K and V caches for fa_decode_int8.  k, v: bf16 [B, S, Hkv, D].  Returns
+    ``(k_codes, v_codes, k_scale, v_scale)``: int8 [B, S, Hkv, D] twice, fp32 [B, Hkv, S] twice
+    (the buffers given, or new ones)."""
+    return _kv_quantize(8, k, v, k_codes, v_codes, k_scale, v_scale, stream)
+
+
+def fa_kv_quantize_int4(k, v, k_codes=None, v_codes=None, k_scale=None, v_scale=None, stream=None):
+    """As fa_kv_quantize_int8 for fa_decode_int4: codes uint8 [B, S, Hkv, D/2], two per byte."""
+    return _kv_quantize(4, k, v, k_codes, v_codes, k_scale, v_scale, stream)
+
+
+def _kv_dequantize(bits, k_codes, v_codes, k_scale, v_scale, k, v, stream):
+    import torch
+    name = f"fa_kv_dequantize_int{bits}"
+    if k_codes.dim() != 4:
+        raise ValueError("k_codes, v_codes must be 4-D [B, S, Hkv, row]")
+    B, S, Hkv, row = k_codes.shape
+    D = row if bits == 8 else 2 * row
+    dev = k_codes.device
+    code, _ = _code_type(bits, D)
+    _check(k_codes, "k_codes", code, (B, S, Hkv, row), dev)
+    _check(v_codes, "v_codes", code, (B, S, Hkv, row), dev)
+    _check(k_scale, "k_scale", torch.float32, (B, Hkv, S), dev)
+    _check(v_scale, "v_scale", torch.float32, (B, Hkv, S), dev)
+    with _on(dev, stream):
+        k = torch.empty((B, S, Hkv, D), dtype=torch.bfloat16, device=dev) if k is None else k
+        v = torch.empty((B, S, Hkv, D), dtype=torch.bfloat16, device=dev) if v is None else v
+        _check(k, "k", torch.bfloat16, (B, S, Hkv, D), dev)
+        _check(v, "v", torch.bfloat16, (B, S, Hkv, D), dev)
+        rc = getattr(lib(), name)(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
+                                  v_scale.data_ptr(), k.data_ptr(), v.data_ptr(), B, S, Hkv, D,
+                                  _stream_ptr(None))
+    if rc != 0:
+        raise FaError(rc, name)
+    return k, v
+
+
+def fa_kv_dequantize_int8(k_codes, v_codes, k_scale, v_scale, k=None, v=None, stream=None):
+    """Read a cache of fa_kv_quantize_int8 back: ``(k, v)`` bf16 [B, S, Hkv, D] = code * scale."""
+    return _kv_dequantize(8, k_codes, v_codes, k_scale, v_scale, k, v, stream)
+
+
+def fa_kv_dequantize_int4(k_codes, v_codes, k_scale, v_scale, k=None, v=None, stream=None):
+    """Read a cache of fa_kv_quantize_int4 back: ``(k, v)`` bf16 [B, S, Hkv, D] = code * scale."""
+    return _kv_dequantize(4, k_codes, v_codes, k_scale, v_scale, k, v, stream)
+
+
+def _check_pool(bits, D, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, dev):
+    """Checks a page pool and a block table; returns (num_pages, P, Hkv, B, max_pages)."""
+    import torch
+    if k_pages.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("k_pages must be [num_pages, P, Hkv, row], block_table [B, max_pages]")
+    num_pages, P, Hkv, _ = k_pages.shape
+    B, max_pages = block_table.shape
+    code, row = _code_type(bits, D)
+    _check(k_pages, "k_pages", code, (num_pages, P, Hkv, row), dev)
+    _check(v_pages, "v_pages", code, (num_pages, P, Hkv, row), dev)
+    _check(k_scale_pages, "k_scale_pages", torch.float32, (num_pages, Hkv, P), dev)
+    _check(v_scale_pages, "v_scale_pages", torch.float32, (num_pages, Hkv, P), dev)
+    _check(block_table, "block_table", torch.int32, (B, max_pages), dev)
+    return num_pages, P, Hkv, B, max_pages
+
+
+def _token_rows(t, name, Hkv, D, dev):
+    """Number of token rows of t ([N, Hkv, D] or [B, T, Hkv, D], each row contiguous, rows evenly
+    spaced) and the elements between them."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a torch.bfloat16 tensor")
+    if t.dim() not in (3, 4) or tuple(t.shape[-2:]) != (Hkv, D):
+        raise ValueError(f"{name} must have shape [N, {Hkv}, {D}] or [B, T, {Hkv}, {D}], got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.numel() == 0:
+        return 0, Hkv * D
+    st = t.stride()
+    if (st[-1] != 1 and D > 1) or (st[-2] != D and Hkv > 1):
+        raise ValueError(f"{name}: each token's [Hkv, D] row must be contiguous")
+    n, step = t.shape[0], st[0]
+    if t.dim() == 4:
+        n, step = t.shape[0] * t.shape[1], st[1]
+        if t.shape[1] == 1:
+            step = st[0]
+        elif t.shape[0] > 1 and st[0] != t.shape[1] * st[1]:
+            raise ValueError(f"{name}: token rows must be evenly spaced")
+    return n, (step if n > 1 else max(step, Hkv * D))
+
+
+def _kv_append(bits, k, v, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, positions,
+               cu_tokens, stream):
+    import torch
+    name = f"fa_kv_append_int{bits}_paged"
+    dev, D = k.device, k.shape[-1]
+    num_pages, P, Hkv, B, max_pages = _check_pool(bits, D, k_pages, v_pages, k_scale_pages,
+                                                  v_scale_pages, block_table, dev)
+    n, k_stride = _token_rows(k, "k", Hkv, D, dev)
+    nv, v_stride = _token_rows(v, "v", Hkv, D, dev)
+    if v.shape != k.shape:
+        raise ValueError(f"v must have shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    if positions is not None:
+        _check(positions, "positions", torch.int32, (B,), dev)
+    if cu_tokens is not None:
+        _check(cu_tokens, "cu_tokens", torch.int32, (B + 1,), dev)
+    elif k.dim() == 4 and k.shape[0] != B:
+        raise ValueError(f"k must hold {B} sequences, got {k.shape[0]}")
+    with _on(dev, stream):
+        rc = getattr(lib(), name)(
+            k.data_ptr(), v.data_ptr(), k_stride, v_stride, k_pages.data_ptr(), v_pages.data_ptr(),
+            k_scale_pages.data_ptr(), v_scale_pages.data_ptr(), block_table.data_ptr(),
+            positions.data_ptr() if positions is not None else None,
+            cu_tokens.data_ptr() if cu_tokens is not None else None, n, B, Hkv, P, max_pages,
+            num_pages, D, _stream_ptr(None))
+    if rc != 0:
+        raise FaError(rc, name)
+
+
+def fa_kv_append_int8_paged(k, v, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table,
+                            positions=None, cu_tokens=None, stream=None):
+    """Quantise new tokens into a paged INT8 cache (the layout of fa_decode_int8_paged), in place.
+    k, v: bf16 [N, Hkv, D] or [B, T, Hkv, D]; token rows may be strided (slices of one projection's
+    output).  positions: int32 [B], each sequence's length before the call (None: 0).  cu_tokens:
+    int32 [B + 1], first row of each sequence's new tokens (None: the same number of each)."""
+    _kv_append(8, k, v, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, positions,
+               cu_tokens, stream)
+
+
+def fa_kv_append_int4_paged(k, v, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table,
+                            positions=None, cu_tokens=None, stream=None):
+    """As fa_kv_append_int8_paged into uint8 [num_pages, P, Hkv, D/2] pages of fa_decode_int4_paged."""
+    _kv_append(4, k, v, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, positions,
+               cu_tokens, stream)
+
+
+def _kv_gather(bits, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, num_tokens,
+               positions, cu_tokens, k, v, stream):
+    import torch
+    name = f"fa_kv_gather_int{bits}_paged"
+    dev = k_pages.device
+    D = k_pages.shape[-1] * (1 if bits == 8 else 2)
+    num_pages, P, Hkv, B, max_pages = _check_pool(bits, D, k_pages, v_pages, k_scale_pages,
+                                                  v_scale_pages, block_table, dev)
+    if positions is not None:
+        _check(positions, "positions", torch.int32, (B,), dev)
+    if cu_tokens is not None:
+        _check(cu_tokens, "cu_tokens", torch.int32, (B + 1,), dev)
+    n = int(num_tokens)
+    if n < 0:
+        raise ValueError(f"num_tokens must not be negative, got {n}")
+    with _on(dev, stream):
+        k = torch.empty((n, Hkv, D), dtype=torch.bfloat16, device=dev) if k is None else k
+        v = torch.empty((n, Hkv, D), dtype=torch.bfloat16, device=dev) if v is None else v
+        _check(k, "k", torch.bfloat16, (n, Hkv, D), dev)
+        _check(v, "v", torch.bfloat16, (n, Hkv, D), dev)
+        rc = getattr(lib(), name)(
+            k_pages.data_ptr(), v_pages.data_ptr(), k_scale_pages.data_ptr(),
+            v_scale_pages.data_ptr(), block_table.data_ptr(),
+            positions.data_ptr() if positions is not None else None,
+            cu_tokens.data_ptr() if cu_tokens is not None else None, k.data_ptr(), v.data_ptr(),
+            n, B, Hkv, P, max_pages, num_pages, D, _stream_ptr(None))
+    if rc != 0:
+        raise FaError(rc, name)
+    return k, v
+
+
+def fa_kv_gather_int8_paged(k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, num_tokens,
+                            positions=None, cu_tokens=None, k=None, v=None, stream=None):
+    """Read ``num_tokens`` tokens of a paged INT8 cache back as ``(k, v)``, bf16 [num_tokens, Hkv, D]
+    each: row cu_tokens[b] + i is position positions[b] + i of sequence b (positions None: 0;
+    cu_tokens None: num_tokens / B of each sequence).  Rows behind cu_tokens[B] are left as they
+    were (undefined in new buffers)."""
+    return _kv_gather(8, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, num_tokens,
+                      positions, cu_tokens, k, v, stream)
+
+
+def fa_kv_gather_int4_paged(k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, num_tokens,
+                            positions=None, cu_tokens=None, k=None, v=None, stream=None):
+    """As fa_kv_gather_int8_paged from a paged INT4 cache."""
+    return _kv_gather(4, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, num_tokens,
+                      positions, cu_tokens, k, v, stream)
 
 
 def fa_device_status(stream=None) -> int:

@@ -13,6 +13,7 @@
 #include "../../include/fa.h"
 #include "backward.cuh"
 #include "decode.cuh"
+#include "kvcache.cuh"
 #include "prefill.cuh"
 #include "sm100.cuh"
 
@@ -483,6 +484,109 @@ int decode_paged(int bits, const void* q, const void* k, const void* v, const fl
                                                 splits, ws, st);
 }
 
+int page_shift_of(int page_size) {
+  for (int s = 4; s <= 16; ++s)
+    if (page_size == (1 << s)) return s;
+  return -1;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// One warp per (32 tokens, K or V, KV head), 8 warps per block.
+template <int D, int kBits, bool kPaged, bool kWrite>
+int launch_kv_copy(const fa::KvCopyParams& p, cudaStream_t stream) {
+  const long long units = (static_cast<long long>(p.map.N) + 31) / 32 * 2 * p.map.Hkv;
+  const long long grid = (units + 7) / 8;
+  if (grid > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  if (kWrite)
+    fa::fa_kv_write_kernel<D, kBits, kPaged><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
+  else
+    fa::fa_kv_read_kernel<D, kBits, kPaged><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int kBits, bool kPaged, bool kWrite>
+int launch_kv_copy_d(const fa::KvCopyParams& p, int D, cudaStream_t stream) {
+  return D == 128 ? launch_kv_copy<128, kBits, kPaged, kWrite>(p, stream)
+                  : launch_kv_copy<64, kBits, kPaged, kWrite>(p, stream);
+}
+
+// A whole contiguous cache, written from (or read back to) bf16 [B, Skv, Hkv, D].
+template <int kBits, bool kWrite>
+int kv_contiguous(const void* k, const void* v, const void* kc, const void* vc, const float* ks,
+                  const float* vs, int B, int Skv, int Hkv, int D, void* stream) {
+  if (!k || !v || !kc || !vc || !ks || !vs) return FA_ERR_INVALID_ARG;
+  if (B <= 0 || Skv <= 0 || Hkv <= 0 || D <= 0) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * Skv > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(kc) || !aligned16(vc) || !aligned16(ks) ||
+      !aligned16(vs))
+    return FA_ERR_ALIGNMENT;
+  fa::KvCopyParams p{};
+  p.map.N = B * Skv;
+  p.map.B = B;
+  p.map.per_seq = Skv;
+  p.map.Hkv = Hkv;
+  p.map.page_size = Skv;
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.k_out = static_cast<uint16_t*>(const_cast<void*>(k));
+  p.v_out = static_cast<uint16_t*>(const_cast<void*>(v));
+  p.k_stride = p.v_stride = static_cast<long long>(Hkv) * D;
+  p.k_codes = static_cast<uint8_t*>(const_cast<void*>(kc));
+  p.v_codes = static_cast<uint8_t*>(const_cast<void*>(vc));
+  p.k_scale = const_cast<float*>(ks);
+  p.v_scale = const_cast<float*>(vs);
+  return launch_kv_copy_d<kBits, false, kWrite>(p, D, static_cast<cudaStream_t>(stream));
+}
+
+// Tokens of a paged cache, written from (or read back to) bf16 [N, Hkv, D].
+template <int kBits, bool kWrite>
+int kv_paged(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const void* kc,
+             const void* vc, const float* ks, const float* vs, const int32_t* block_table,
+             const int32_t* positions, const int32_t* cu_tokens, int N, int B, int Hkv,
+             int page_size, int max_pages, int num_pages, int D, void* stream) {
+  if (!kc || !vc || !ks || !vs || !block_table) return FA_ERR_INVALID_ARG;
+  if (N < 0 || B <= 0 || Hkv <= 0 || D <= 0 || max_pages <= 0 || num_pages <= 0)
+    return FA_ERR_INVALID_ARG;
+  if (!cu_tokens && N % B != 0) return FA_ERR_INVALID_ARG;
+  const int shift = page_shift_of(page_size);
+  if (shift < 0 || (static_cast<long long>(max_pages) << shift) > (1ll << 30))
+    return FA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (!aligned16(kc) || !aligned16(vc) || !aligned16(ks) || !aligned16(vs) ||
+      !aligned4(block_table) || !aligned4(positions) || !aligned4(cu_tokens))
+    return FA_ERR_ALIGNMENT;
+  if (N == 0) return FA_OK;
+  const int64_t row = static_cast<int64_t>(Hkv) * D;
+  if (!k || !v || k_stride < row || v_stride < row) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return FA_ERR_ALIGNMENT;
+  fa::KvCopyParams p{};
+  p.map.cu_tokens = cu_tokens;
+  p.map.positions = positions;
+  p.map.block_table = block_table;
+  p.map.N = N;
+  p.map.B = B;
+  p.map.per_seq = cu_tokens ? 0 : N / B;
+  p.map.Hkv = Hkv;
+  p.map.page_size = page_size;
+  p.map.page_shift = shift;
+  p.map.max_pages = max_pages;
+  p.map.num_pages = num_pages;
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.k_out = static_cast<uint16_t*>(const_cast<void*>(k));
+  p.v_out = static_cast<uint16_t*>(const_cast<void*>(v));
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.k_codes = static_cast<uint8_t*>(const_cast<void*>(kc));
+  p.v_codes = static_cast<uint8_t*>(const_cast<void*>(vc));
+  p.k_scale = const_cast<float*>(ks);
+  p.v_scale = const_cast<float*>(vs);
+  return launch_kv_copy_d<kBits, true, kWrite>(p, D, static_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -651,6 +755,74 @@ int fa_decode_int4_paged(const void* q, const uint8_t* k_pages, const uint8_t* v
   return decode_paged(4, q, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, seqlens,
                       o, lse, B, Hq, Hkv, page_size, max_pages_per_seq, num_pages, D, scale,
                       num_splits, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int fa_kv_quantize_int8(const void* k, const void* v, int8_t* k_codes, int8_t* v_codes,
+                         float* k_scale, float* v_scale, int B, int Skv, int Hkv, int D,
+                         void* stream) {
+  return kv_contiguous<8, true>(k, v, k_codes, v_codes, k_scale, v_scale, B, Skv, Hkv, D, stream);
+}
+
+int fa_kv_dequantize_int8(const int8_t* k_codes, const int8_t* v_codes, const float* k_scale,
+                           const float* v_scale, void* k, void* v, int B, int Skv, int Hkv, int D,
+                           void* stream) {
+  return kv_contiguous<8, false>(k, v, k_codes, v_codes, k_scale, v_scale, B, Skv, Hkv, D, stream);
+}
+
+int fa_kv_append_int8_paged(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                             int8_t* k_pages, int8_t* v_pages, float* k_scale_pages,
+                             float* v_scale_pages, const int32_t* block_table,
+                             const int32_t* positions, const int32_t* cu_tokens, int num_tokens,
+                             int B, int Hkv, int page_size, int max_pages_per_seq, int num_pages,
+                             int D, void* stream) {
+  return kv_paged<8, true>(k, v, k_stride, v_stride, k_pages, v_pages, k_scale_pages, v_scale_pages,
+                           block_table, positions, cu_tokens, num_tokens, B, Hkv, page_size,
+                           max_pages_per_seq, num_pages, D, stream);
+}
+
+int fa_kv_gather_int8_paged(const int8_t* k_pages, const int8_t* v_pages, const float* k_scale_pages,
+                             const float* v_scale_pages, const int32_t* block_table,
+                             const int32_t* positions, const int32_t* cu_tokens, void* k, void* v,
+                             int num_tokens, int B, int Hkv, int page_size, int max_pages_per_seq,
+                             int num_pages, int D, void* stream) {
+  const int64_t row = static_cast<int64_t>(Hkv) * D;
+  return kv_paged<8, false>(k, v, row, row, k_pages, v_pages, k_scale_pages, v_scale_pages,
+                            block_table, positions, cu_tokens, num_tokens, B, Hkv, page_size,
+                            max_pages_per_seq, num_pages, D, stream);
+}
+
+int fa_kv_quantize_int4(const void* k, const void* v, uint8_t* k_codes, uint8_t* v_codes,
+                         float* k_scale, float* v_scale, int B, int Skv, int Hkv, int D,
+                         void* stream) {
+  return kv_contiguous<4, true>(k, v, k_codes, v_codes, k_scale, v_scale, B, Skv, Hkv, D, stream);
+}
+
+int fa_kv_dequantize_int4(const uint8_t* k_codes, const uint8_t* v_codes, const float* k_scale,
+                           const float* v_scale, void* k, void* v, int B, int Skv, int Hkv, int D,
+                           void* stream) {
+  return kv_contiguous<4, false>(k, v, k_codes, v_codes, k_scale, v_scale, B, Skv, Hkv, D, stream);
+}
+
+int fa_kv_append_int4_paged(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                             uint8_t* k_pages, uint8_t* v_pages, float* k_scale_pages,
+                             float* v_scale_pages, const int32_t* block_table,
+                             const int32_t* positions, const int32_t* cu_tokens, int num_tokens,
+                             int B, int Hkv, int page_size, int max_pages_per_seq, int num_pages,
+                             int D, void* stream) {
+  return kv_paged<4, true>(k, v, k_stride, v_stride, k_pages, v_pages, k_scale_pages, v_scale_pages,
+                           block_table, positions, cu_tokens, num_tokens, B, Hkv, page_size,
+                           max_pages_per_seq, num_pages, D, stream);
+}
+
+int fa_kv_gather_int4_paged(const uint8_t* k_pages, const uint8_t* v_pages, const float* k_scale_pages,
+                             const float* v_scale_pages, const int32_t* block_table,
+                             const int32_t* positions, const int32_t* cu_tokens, void* k, void* v,
+                             int num_tokens, int B, int Hkv, int page_size, int max_pages_per_seq,
+                             int num_pages, int D, void* stream) {
+  const int64_t row = static_cast<int64_t>(Hkv) * D;
+  return kv_paged<4, false>(k, v, row, row, k_pages, v_pages, k_scale_pages, v_scale_pages,
+                            block_table, positions, cu_tokens, num_tokens, B, Hkv, page_size,
+                            max_pages_per_seq, num_pages, D, stream);
 }
 
 int fa_selftest_bounded_wait(int timeout_us, void* stream) {
