@@ -398,3 +398,22 @@ def test_graph_and_side_stream(built):
             assert same_values(_bits(out[w]), values_bits(*quantize_f64(x[w], 127)))
     want = [p.copy() for p in pool]
     assert fa.fa_device_status() == 0 and want[0].shape == tuple(dev["pool"][0].shape)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("S,splits", [(5, 1), (300, 2), (300, 16)])
+def test_decode_of_a_row_written_from_nan_is_nan(built, bits, S, splits):
+    """K (then V) of one token of KV head 1 holds a NaN: the heads that read it are NaN, the others are not."""
+    import torch
+    B, Hq, Hkv, D = 2, 12, 3, 64
+    k, v, q = (_bf16(make_rows(s, (B, n, h, D), "normal")) for s, n, h in ((1, S, Hkv), (2, S, Hkv), (3, 1, Hq)))
+    for x in (k, v):
+        kept = x[1, 2, 1].clone()
+        x[1, 2, 1, 9] = float("nan")
+        cache = _call("quantize", bits)(k, v)
+        o, lse = getattr(fa, f"fa_decode_int{bits}")(q, *cache, num_splits=splits)
+        assert torch.isnan(o[1, 0, 4:8]).all() and torch.isnan(lse[1, 4:8]).all() == (x is k)
+        o[1, 0, 4:8], lse[1, 4:8] = 0, 0
+        assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+        x[1, 2, 1] = kept

@@ -713,19 +713,18 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < 4; ++w) M = fmaxf(M, sm_m[w * 8 + h]);
+    // a sum of 0 means no key; a NaN among the scales (a row written from a NaN) stays one
     float L = 0.f, acc = 0.f;
-    if (M != -INFINITY) {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float mw = sm_m[w * 8 + h];
-        const float f = (mw == -INFINITY) ? 0.f : ex2(mw - M);
-        L += f * sm_l[w * 8 + h];
-        acc += f * sm_o[(w * 8 + h) * D + d];
-      }
+    for (int w = 0; w < 4; ++w) {
+      const float mw = sm_m[w * 8 + h];
+      const float f = (mw == -INFINITY) ? 0.f : ex2(mw - M);
+      L += f * sm_l[w * 8 + h];
+      acc += f * sm_o[(w * 8 + h) * D + d];
     }
     const size_t row = (static_cast<size_t>(split) * p.B + b) * p.Hq + head0 + h;
-    p.o_part[row * D + d] = (L > 0.f) ? acc / L : 0.f;
-    if (d == 0) p.lse_part[row] = (L > 0.f) ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+    p.o_part[row * D + d] = (L == 0.f) ? 0.f : acc / L;
+    if (d == 0) p.lse_part[row] = (L == 0.f) ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
   }
 }
 
@@ -751,32 +750,30 @@ __global__ void __launch_bounds__(128) fa_decode_combine_kernel(const CombinePar
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  if (M != -INFINITY) {
-    for (int s = lane; s < p.splits; s += 32) {
-      const float ls = p.lse_part[s * stride + row];
-      L += (ls == -INFINITY) ? 0.f : expf(ls - M);
-    }
+  for (int s = lane; s < p.splits; s += 32) {
+    const float ls = p.lse_part[s * stride + row];
+    L += (ls == -INFINITY) ? 0.f : expf(ls - M);
+  }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
 #pragma unroll 4
-    for (int s = 0; s < p.splits; ++s) {
-      const float ls = p.lse_part[s * stride + row];
-      const float w = (ls == -INFINITY) ? 0.f : expf(ls - M);
-      const float* src = p.o_part + (s * stride + row) * D + V * lane;
-      if constexpr (V == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        acc[0] += w * x.x;
-        acc[1 % V] += w * x.y;
-        acc[2 % V] += w * x.z;
-        acc[3 % V] += w * x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        acc[0] += w * x.x;
-        acc[1 % V] += w * x.y;
-      }
+  for (int s = 0; s < p.splits; ++s) {
+    const float ls = p.lse_part[s * stride + row];
+    const float w = (ls == -INFINITY) ? 0.f : expf(ls - M);
+    const float* src = p.o_part + (s * stride + row) * D + V * lane;
+    if constexpr (V == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      acc[0] += w * x.x;
+      acc[1 % V] += w * x.y;
+      acc[2 % V] += w * x.z;
+      acc[3 % V] += w * x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(src);
+      acc[0] += w * x.x;
+      acc[1 % V] += w * x.y;
     }
   }
-  const float inv = (L > 0.f) ? 1.f / L : 0.f;
+  const float inv = (L == 0.f) ? 0.f : 1.f / L;
   uint16_t* dst = p.o + static_cast<size_t>(row) * D + V * lane;
   if constexpr (V == 4) {
     uint2 w2;
@@ -786,7 +783,7 @@ __global__ void __launch_bounds__(128) fa_decode_combine_kernel(const CombinePar
   } else {
     *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1 % V] * inv);
   }
-  if (lane == 0 && p.lse != nullptr) p.lse[row] = (L > 0.f) ? M + logf(L) : -INFINITY;
+  if (lane == 0 && p.lse != nullptr) p.lse[row] = (L == 0.f) ? -INFINITY : M + logf(L);
 }
 
 }  // namespace fa
