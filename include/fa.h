@@ -358,6 +358,56 @@ FA_API int fa_kv_gather_int4_paged(const uint8_t* k_pages, const uint8_t* v_page
                                    int B, int Hkv, int page_size, int max_pages_per_seq,
                                    int num_pages, int D, void* stream);
 
+/*
+ * Decode step of a batch that shares a prefix (a system prompt, a document, the prompt of several
+ * samples): one query token per sequence attends to the prefix's keys and to its sequence's own
+ * keys, all in one paged INT8 cache (sources: block_table and lengths as for fa_decode_int8_paged).
+ * The result is that of fa_decode_int8_paged over tables that begin with the prefix's pages, but
+ * the prefix is read and multiplied once for the whole batch.
+ *   q, o, lse, k_pages, v_pages, k_scale_pages, v_scale_pages, page_size, num_pages, scale
+ *                 as for fa_decode_int8_paged.
+ *   prefix_table  int32 [max_prefix_pages] (device): key j of the prefix is row j % page_size of
+ *                 page prefix_table[j / page_size].  Entries past the prefix's last page are never
+ *                 read.
+ *   prefix_len    int32 [1] (device): keys of the prefix, 0 .. max_prefix_pages * page_size; it may
+ *                 end inside a page (that page's other rows are not read as keys).
+ *   block_table, seqlens  as for fa_decode_int8_paged, of each sequence's own keys, which follow
+ *                 the prefix; a length may be 0.  A sequence that sees no key at all gets O = 0 and
+ *                 LSE = -inf.
+ *   max_prefix_pages, max_pages_per_seq  times page_size at most 2^30 each.
+ *   num_splits    splits of the own keys as for fa_decode_int8_paged, or 0: the library chooses.  How
+ *                 the prefix is split follows from the sizes.
+ *   workspace     at least fa_decode_shared_workspace_bytes(B, Hq, Hkv, D, max_prefix_pages *
+ *                 page_size, max_pages_per_seq * page_size, num_splits) bytes, 16-byte aligned;
+ *                 contents on entry do not matter.  Calls that may run at the same time must not
+ *                 share one.
+ * Alignment and the device-side checks of lengths and page ids are those of fa_decode_int8_paged.
+ * A NaN among the scales (a row written from a NaN) makes every row that reads it NaN, and no other.
+ * D must be 64 or 128; Hq must be a multiple of Hkv; B * ceil(Hq / Hkv / 8) <= 65535.
+ * fa_decode_shared_workspace_bytes returns 0 for invalid sizes.
+ */
+FA_API size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int D, int max_prefix_len,
+                                               int max_seqlen, int num_splits);
+FA_API int fa_decode_int8_shared(const void* q, const int8_t* k_pages, const int8_t* v_pages,
+                                 const float* k_scale_pages, const float* v_scale_pages,
+                                 const int32_t* prefix_table, const int32_t* prefix_len,
+                                 const int32_t* block_table, const int32_t* seqlens, void* o,
+                                 float* lse, int B, int Hq, int Hkv, int page_size,
+                                 int max_prefix_pages, int max_pages_per_seq, int num_pages, int D,
+                                 float scale, int num_splits, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* The same over an INT4 cache: k_pages, v_pages uint8 [num_pages, page_size, Hkv, D/2] packed as for
+ * fa_decode_int4. */
+FA_API int fa_decode_int4_shared(const void* q, const uint8_t* k_pages, const uint8_t* v_pages,
+                                 const float* k_scale_pages, const float* v_scale_pages,
+                                 const int32_t* prefix_table, const int32_t* prefix_len,
+                                 const int32_t* block_table, const int32_t* seqlens, void* o,
+                                 float* lse, int B, int Hq, int Hkv, int page_size,
+                                 int max_prefix_pages, int max_pages_per_seq, int num_pages, int D,
+                                 float scale, int num_splits, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
 /* Static, human-readable name of a status code.  Never NULL. */
 FA_API const char* fa_status_string(int status);
 

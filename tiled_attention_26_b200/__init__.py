@@ -17,7 +17,8 @@ __all__ = ["FaError", "lib", "fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_d
            "fa_decode_int4", "fa_decode_int4_paged", "fa_decode_int8_workspace_bytes",
            "fa_kv_quantize_int8", "fa_kv_quantize_int4", "fa_kv_dequantize_int8", "fa_kv_dequantize_int4",
            "fa_kv_append_int8_paged", "fa_kv_append_int4_paged", "fa_kv_gather_int8_paged",
-           "fa_kv_gather_int4_paged",
+           "fa_kv_gather_int4_paged", "fa_decode_int8_shared", "fa_decode_int4_shared",
+           "fa_decode_shared_workspace_bytes",
            "fa_status_string", "fa_device_status", "fa_selftest_bounded_wait", "LIB_PATH",
            "STATUS"]
 
@@ -85,6 +86,10 @@ def lib() -> ctypes.CDLL:
             f.restype = _I
             f = getattr(L, f"fa_kv_gather_int{bits}_paged")
             f.argtypes, f.restype = [_P] * 9 + [_I] * 7 + [_P], _I
+            f = getattr(L, f"fa_decode_int{bits}_shared")
+            f.argtypes, f.restype = [_P] * 11 + [_I] * 8 + [_F, _I, _P, _Z, _P], _I
+        L.fa_decode_shared_workspace_bytes.argtypes = [_I] * 7
+        L.fa_decode_shared_workspace_bytes.restype = _Z
         L.fa_status_string.argtypes = [_I]
         L.fa_status_string.restype = ctypes.c_char_p
         L.fa_device_status.argtypes = [_P]
@@ -425,13 +430,13 @@ def fa_kv_dequantize_int4(k_codes, v_codes, k_scale, v_scale, k=None, v=None, st
     return _kv_dequantize(4, k_codes, v_codes, k_scale, v_scale, k, v, stream)
 
 
-def _check_pool(bits, D, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, dev):
+def _check_pool(bits, D, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, dev, B=None):
     """Checks a page pool and a block table; returns (num_pages, P, Hkv, B, max_pages)."""
     import torch
     if k_pages.dim() != 4 or block_table.dim() != 2:
         raise ValueError("k_pages must be [num_pages, P, Hkv, row], block_table [B, max_pages]")
     num_pages, P, Hkv, _ = k_pages.shape
-    B, max_pages = block_table.shape
+    B, max_pages = (block_table.shape[0] if B is None else B), block_table.shape[1]
     code, row = _code_type(bits, D)
     _check(k_pages, "k_pages", code, (num_pages, P, Hkv, row), dev)
     _check(v_pages, "v_pages", code, (num_pages, P, Hkv, row), dev)
@@ -557,6 +562,79 @@ def fa_kv_gather_int4_paged(k_pages, v_pages, k_scale_pages, v_scale_pages, bloc
     """As fa_kv_gather_int8_paged from a paged INT4 cache."""
     return _kv_gather(4, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, num_tokens,
                       positions, cu_tokens, k, v, stream)
+
+
+def fa_decode_shared_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, max_prefix_len: int,
+                                     max_seqlen: int, num_splits: int = 0) -> int:
+    return int(lib().fa_decode_shared_workspace_bytes(B, Hq, Hkv, D, max_prefix_len, max_seqlen,
+                                                      num_splits))
+
+
+def _decode_shared(bits, q, k_pages, v_pages, k_scale_pages, v_scale_pages, prefix_table,
+                   prefix_len, block_table, seqlens, num_splits, scale, o, lse, workspace,
+                   return_lse, stream):
+    import torch
+    name = f"fa_decode_int{bits}_shared"
+    if q.dim() != 4 or q.shape[1] != 1:
+        raise ValueError("decode takes one query token per sequence, q [B, 1, Hq, D]")
+    B, _, Hq, D = q.shape
+    dev = q.device
+    _check(q, "q", torch.bfloat16, (B, 1, Hq, D), dev)
+    num_pages, P, Hkv, _, max_pages = _check_pool(bits, D, k_pages, v_pages, k_scale_pages,
+                                                  v_scale_pages, block_table, dev, B)
+    if prefix_table.dim() != 1:
+        raise ValueError("prefix_table must be [max_prefix_pages]")
+    max_prefix = prefix_table.shape[0]
+    _check(prefix_table, "prefix_table", torch.int32, (max_prefix,), dev)
+    _check(prefix_len, "prefix_len", torch.int32, (1,), dev)
+    _check(seqlens, "seqlens", torch.int32, (B,), dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _on(dev, stream):
+        o = torch.empty_like(q) if o is None else o
+        _check(o, "o", torch.bfloat16, (B, 1, Hq, D), dev)
+        if lse is None and return_lse:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        if lse is not None:
+            _check(lse, "lse", torch.float32, (B, Hq), dev)
+        if workspace is None:
+            need = fa_decode_shared_workspace_bytes(B, Hq, Hkv, D, max_prefix * P, max_pages * P,
+                                                    num_splits)
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        rc = getattr(lib(), name)(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale_pages.data_ptr(),
+            v_scale_pages.data_ptr(), prefix_table.data_ptr(), prefix_len.data_ptr(),
+            block_table.data_ptr(), seqlens.data_ptr(), o.data_ptr(),
+            lse.data_ptr() if lse is not None else None, B, Hq, Hkv, P, max_prefix, max_pages,
+            num_pages, D, scale, num_splits, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream_ptr(None))
+    if rc != 0:
+        raise FaError(rc, name)
+    return o, lse
+
+
+def fa_decode_int8_shared(q, k_pages, v_pages, k_scale_pages, v_scale_pages, prefix_table,
+                          prefix_len, block_table, seqlens, num_splits: int = 0,
+                          scale: float | None = None, o=None, lse=None, workspace=None,
+                          return_lse: bool = True, stream=None):
+    """Decode step of a batch that shares a prefix, over a paged INT8 cache.  prefix_table: int32
+    [max_prefix_pages] and prefix_len: int32 [1], the shared keys' pages and number; block_table:
+    int32 [B, max_pages] and seqlens: int32 [B], each sequence's own keys (all on the device).
+    num_splits: splits of the own keys (0: chosen).  Otherwise as fa_decode_int8_paged; returns
+    ``(o, lse)``."""
+    return _decode_shared(8, q, k_pages, v_pages, k_scale_pages, v_scale_pages, prefix_table,
+                          prefix_len, block_table, seqlens, num_splits, scale, o, lse, workspace,
+                          return_lse, stream)
+
+
+def fa_decode_int4_shared(q, k_pages, v_pages, k_scale_pages, v_scale_pages, prefix_table,
+                          prefix_len, block_table, seqlens, num_splits: int = 0,
+                          scale: float | None = None, o=None, lse=None, workspace=None,
+                          return_lse: bool = True, stream=None):
+    """As fa_decode_int8_shared over uint8 [num_pages, P, Hkv, D/2] pages of fa_decode_int4_paged."""
+    return _decode_shared(4, q, k_pages, v_pages, k_scale_pages, v_scale_pages, prefix_table,
+                          prefix_len, block_table, seqlens, num_splits, scale, o, lse, workspace,
+                          return_lse, stream)
 
 
 def fa_device_status(stream=None) -> int:

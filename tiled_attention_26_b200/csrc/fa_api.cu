@@ -15,6 +15,7 @@
 #include "decode.cuh"
 #include "kvcache.cuh"
 #include "prefill.cuh"
+#include "shared_decode.cuh"
 #include "sm100.cuh"
 
 // Scratch of the allocation-free decode entry point: one copy per GPU that loads the library,
@@ -306,12 +307,11 @@ fa::DecodeParams decode_params(const void* q, const int8_t* k, const int8_t* v, 
 
 std::atomic<uint64_t> g_attr_decode[8];
 
-// Split kernel over grid (Hkv, splits, B * head blocks), then the merge kernel.  `keys` is the
-// extent of the key axis of the code tensors (Skv, or the page size), `outer` that of the last
-// axis (B, or the number of pages).
+// Split kernel over grid (Hkv, splits, B * head blocks).  `keys` is the extent of the key axis of
+// the code tensors (Skv, or the page size), `outer` that of the last axis (B, or the number of
+// pages).
 template <int D, bool kPaged, int kBits>
-int launch_split_and_combine(const fa::DecodeParams& p, int keys, int outer, void* o, float* lse,
-                             cudaStream_t stream) {
+int launch_split(const fa::DecodeParams& p, int keys, int outer, cudaStream_t stream) {
   using C = fa::DecodeCfg<D, kBits>;
   const long long gz = static_cast<long long>(p.B) * ((p.G + 7) / 8);
   if (p.splits > 65535 || gz > 65535) return FA_ERR_INVALID_ARG;
@@ -327,7 +327,15 @@ int launch_split_and_combine(const fa::DecodeParams& p, int keys, int outer, voi
   if ((rc = ensure_smem_attr(kernel, C::kSmemBytes, g_attr_decode[variant])) != FA_OK) return rc;
   dim3 grid(p.Hkv, p.splits, static_cast<unsigned>(gz));
   kernel<<<grid, 160, C::kSmemBytes, stream>>>(tk, tv, p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// The split kernel, then the merge kernel.
+template <int D, bool kPaged, int kBits>
+int launch_split_and_combine(const fa::DecodeParams& p, int keys, int outer, void* o, float* lse,
+                             cudaStream_t stream) {
+  const int rc = launch_split<D, kPaged, kBits>(p, keys, outer, stream);
+  if (rc != FA_OK) return rc;
   fa::CombineParams cp{};
   cp.o_part = p.o_part;
   cp.lse_part = p.lse_part;
@@ -484,6 +492,89 @@ int decode_paged(int bits, const void* q, const void* k, const void* v, const fl
                                                 splits, ws, st);
 }
 
+// ---- decode over a shared prefix ----
+
+constexpr int kSms = 148;
+
+// Splits of the prefix: one CTA per SM runs a split of one (KV head, row block) in about
+// (tiles + 3) tile times (start-up, epilogue and its share of the merge count for three), in
+// as many waves as the CTAs need; the split count with the least total time, the smaller of equals.
+int shared_prefix_splits(int B, int Hq, int Hkv, long long max_keys) {
+  const long long R = static_cast<long long>(B) * (Hq / Hkv);
+  const long long base = static_cast<long long>(Hkv) * (R <= 128 ? 1 : (R + 255) / 256);
+  const long long tiles = std::max(1ll, (max_keys + 127) / 128);
+  int best = 1;
+  long long best_cost = -1;
+  for (int s = 1; s <= kSms && s <= tiles; ++s) {
+    const long long cost = (base * s + kSms - 1) / kSms * ((tiles + s - 1) / s + 3);
+    if (best_cost < 0 || cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+// Splits of the sequences' own keys where the caller leaves the choice to the library: as many as
+// fill the SMs (3 CTAs each), no more than there are 128-key stages.
+int shared_own_splits(int B, int Hq, int Hkv, long long max_keys) {
+  const long long ctas = static_cast<long long>(B) * Hkv * ((Hq / Hkv + 7) / 8);
+  return static_cast<int>(std::max(1ll, std::min((3 * kSms + ctas - 1) / ctas, (max_keys + 127) / 128)));
+}
+
+std::atomic<uint64_t> g_attr_shared[8];
+std::atomic<int> g_shared_regs[8] = {};  // registers per thread of each variant, 0 = not read
+
+template <int D, int kBits, bool kStream>
+int launch_shared_prefix(const fa::SharedParams& p, const void* k, const void* v,
+                         cudaStream_t stream) {
+  using C = fa::SharedCfg<D, kBits, kStream>;
+  const long long grid = static_cast<long long>(p.Hkv) * p.row_blocks * p.splits;
+  if (grid > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  CUtensorMap tk, tv;
+  const int page = 1 << p.page_shift;
+  const uint32_t box = static_cast<uint32_t>(std::min(128, page));
+  int rc;
+  if ((rc = encode_u8_4d(&tk, k, C::kRow, p.Hkv, page, p.num_pages, box)) != FA_OK) return rc;
+  if ((rc = encode_u8_4d(&tv, v, C::kRow, p.Hkv, page, p.num_pages, box)) != FA_OK) return rc;
+  auto kernel = fa::fa_shared_prefix_kernel<D, kBits, kStream>;
+  constexpr int variant = (D == 128 ? 4 : 0) + (kBits == 4 ? 2 : 0) + (kStream ? 1 : 0);
+  if ((rc = ensure_smem_attr(kernel, C::kSmemBytes, g_attr_shared[variant])) != FA_OK) return rc;
+  // setmaxnreg redistributes the launch's registers; it only completes if they cover the split
+  int regs = g_shared_regs[variant].load(std::memory_order_acquire);
+  if (regs == 0) {
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess) return FA_ERR_CUDA;
+    regs = attr.numRegs;
+    g_shared_regs[variant].store(regs, std::memory_order_release);
+  }
+  if (regs < C::kLaunchRegs) return FA_ERR_UNSUPPORTED;
+  kernel<<<static_cast<unsigned>(grid), C::kThreads, C::kSmemBytes, stream>>>(tk, tv, p);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int D, int kBits>
+int launch_shared(fa::DecodeParams own, fa::SharedParams sp, void* o, float* lse,
+                  cudaStream_t stream) {
+  // the own keys' partials come first, those of the prefix behind them
+  int rc = launch_split<D, true, kBits>(own, 1 << own.page_shift, own.num_pages, stream);
+  if (rc != FA_OK) return rc;
+  rc = sp.R <= 128 ? launch_shared_prefix<D, kBits, true>(sp, own.k, own.v, stream)
+                   : launch_shared_prefix<D, kBits, false>(sp, own.k, own.v, stream);
+  if (rc != FA_OK) return rc;
+  fa::CombineParams cp{};
+  cp.o_part = own.o_part;
+  cp.lse_part = own.lse_part;
+  cp.o = static_cast<uint16_t*>(o);
+  cp.lse = lse;
+  cp.B = own.B;
+  cp.Hq = own.Hq;
+  cp.splits = own.splits + sp.splits;
+  const long long rows = static_cast<long long>(own.B) * own.Hq;
+  fa::fa_shared_combine_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(cp);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 int page_shift_of(int page_size) {
   for (int s = 4; s <= 16; ++s)
     if (page_size == (1 << s)) return s;
@@ -585,6 +676,81 @@ int kv_paged(const void* k, const void* v, int64_t k_stride, int64_t v_stride, c
   p.k_scale = const_cast<float*>(ks);
   p.v_scale = const_cast<float*>(vs);
   return launch_kv_copy_d<kBits, true, kWrite>(p, D, static_cast<cudaStream_t>(stream));
+}
+
+// Sizes of a shared decode call that the workspace depends on; false if they are not valid.
+bool shared_splits(int B, int Hq, int Hkv, int D, long long max_prefix, long long max_own,
+                   int num_splits, int* own, int* prefix) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0 || max_prefix <= 0 || max_own <= 0 ||
+      num_splits < 0)
+    return false;
+  if (static_cast<long long>(B) * Hq > 0x7fffffffLL) return false;
+  *own = num_splits > 0 ? num_splits : shared_own_splits(B, Hq, Hkv, max_own);
+  *prefix = shared_prefix_splits(B, Hq, Hkv, max_prefix);
+  return *own <= 65535;
+}
+
+int decode_shared(int bits, const void* q, const void* k, const void* v, const float* ks,
+                  const float* vs, const int32_t* prefix_table, const int32_t* prefix_len,
+                  const int32_t* block_table, const int32_t* seqlens, void* o, float* lse, int B,
+                  int Hq, int Hkv, int page_size, int max_prefix_pages, int max_pages,
+                  int num_pages, int D, float scale, int num_splits, void* ws, size_t ws_bytes,
+                  void* stream) {
+  if (!q || !k || !v || !ks || !vs || !prefix_table || !prefix_len || !block_table || !seqlens || !o)
+    return FA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  const int shift = page_shift_of(page_size);
+  if (shift < 0 || max_prefix_pages <= 0 || max_pages <= 0 || num_pages <= 0)
+    return FA_ERR_INVALID_ARG;
+  const long long max_prefix = static_cast<long long>(max_prefix_pages) << shift;
+  const long long max_own = static_cast<long long>(max_pages) << shift;
+  if (max_prefix > (1ll << 30) || max_own > (1ll << 30)) return FA_ERR_INVALID_ARG;
+  int own = 0, prefix = 0;
+  if (!shared_splits(B, Hq, Hkv, D, max_prefix, max_own, num_splits, &own, &prefix))
+    return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * ((Hq / Hkv + 7) / 8) > 65535) return FA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(ks) ||
+      !aligned16(vs) || !aligned4(prefix_table) || !aligned4(prefix_len) ||
+      !aligned4(block_table) || !aligned4(seqlens) || !aligned4(lse))
+    return FA_ERR_ALIGNMENT;
+  const int rc = check_workspace(B, Hq, D, own + prefix, ws, ws_bytes);
+  if (rc != FA_OK) return rc;
+  size_t lse_off = 0;
+  decode_ws_layout(B, Hq, D, own + prefix, &lse_off);
+  fa::DecodeParams dp = decode_params(q, static_cast<const int8_t*>(k),
+                                      static_cast<const int8_t*>(v), ks, vs, B, Hq, Hkv, D, scale,
+                                      own, ws);
+  dp.lse_part = reinterpret_cast<float*>(static_cast<char*>(ws) + lse_off);
+  dp.block_table = block_table;
+  dp.seqlens = seqlens;
+  dp.max_pages = max_pages;
+  dp.num_pages = num_pages;
+  dp.page_shift = shift;
+  fa::SharedParams sp{};
+  sp.q = dp.q;
+  sp.k_scale = ks;
+  sp.v_scale = vs;
+  sp.table = prefix_table;
+  sp.len = prefix_len;
+  sp.o_part = dp.o_part + static_cast<size_t>(own) * B * Hq * D;
+  sp.lse_part = dp.lse_part + static_cast<size_t>(own) * B * Hq;
+  sp.B = B;
+  sp.Hq = Hq;
+  sp.Hkv = Hkv;
+  sp.G = Hq / Hkv;
+  sp.R = B * sp.G;
+  sp.row_blocks = sp.R <= 128 ? 1 : (sp.R + 255) / 256;
+  sp.splits = prefix;
+  sp.max_pages = max_prefix_pages;
+  sp.num_pages = num_pages;
+  sp.page_shift = shift;
+  sp.scale_log2 = dp.scale_log2;
+  sp.timeout_ns = kKernelTimeoutNs;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (D == 128)
+    return bits == 8 ? launch_shared<128, 8>(dp, sp, o, lse, s) : launch_shared<128, 4>(dp, sp, o, lse, s);
+  return bits == 8 ? launch_shared<64, 8>(dp, sp, o, lse, s) : launch_shared<64, 4>(dp, sp, o, lse, s);
 }
 
 }  // namespace
@@ -823,6 +989,39 @@ int fa_kv_gather_int4_paged(const uint8_t* k_pages, const uint8_t* v_pages, cons
   return kv_paged<4, false>(k, v, row, row, k_pages, v_pages, k_scale_pages, v_scale_pages,
                             block_table, positions, cu_tokens, num_tokens, B, Hkv, page_size,
                             max_pages_per_seq, num_pages, D, stream);
+}
+
+size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int D, int max_prefix_len,
+                                        int max_seqlen, int num_splits) {
+  int own = 0, prefix = 0;
+  if (!shared_splits(B, Hq, Hkv, D, max_prefix_len, max_seqlen, num_splits, &own, &prefix)) return 0;
+  return decode_ws_layout(B, Hq, D, own + prefix, nullptr);
+}
+
+int fa_decode_int8_shared(const void* q, const int8_t* k_pages, const int8_t* v_pages,
+                          const float* k_scale_pages, const float* v_scale_pages,
+                          const int32_t* prefix_table, const int32_t* prefix_len,
+                          const int32_t* block_table, const int32_t* seqlens, void* o, float* lse,
+                          int B, int Hq, int Hkv, int page_size, int max_prefix_pages,
+                          int max_pages_per_seq, int num_pages, int D, float scale, int num_splits,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return decode_shared(8, q, k_pages, v_pages, k_scale_pages, v_scale_pages, prefix_table, prefix_len,
+                       block_table, seqlens, o, lse, B, Hq, Hkv, page_size, max_prefix_pages,
+                       max_pages_per_seq, num_pages, D, scale, num_splits, workspace,
+                       workspace_bytes, stream);
+}
+
+int fa_decode_int4_shared(const void* q, const uint8_t* k_pages, const uint8_t* v_pages,
+                          const float* k_scale_pages, const float* v_scale_pages,
+                          const int32_t* prefix_table, const int32_t* prefix_len,
+                          const int32_t* block_table, const int32_t* seqlens, void* o, float* lse,
+                          int B, int Hq, int Hkv, int page_size, int max_prefix_pages,
+                          int max_pages_per_seq, int num_pages, int D, float scale, int num_splits,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return decode_shared(4, q, k_pages, v_pages, k_scale_pages, v_scale_pages, prefix_table, prefix_len,
+                       block_table, seqlens, o, lse, B, Hq, Hkv, page_size, max_prefix_pages,
+                       max_pages_per_seq, num_pages, D, scale, num_splits, workspace,
+                       workspace_bytes, stream);
 }
 
 int fa_selftest_bounded_wait(int timeout_us, void* stream) {

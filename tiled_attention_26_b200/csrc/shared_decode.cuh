@@ -1,0 +1,773 @@
+// Decode attention over a prefix that every sequence of the batch shares.
+//
+// One query token per sequence, B sequences, G query heads per KV head: the R = B * G query rows
+// of a KV head all attend to the same prefix keys, so the prefix part of the attention is a
+// matrix product with R rows per staged K/V tile instead of G, and the cache is read once instead
+// of B times:
+//   x_rj = scale * k_scale_j * (q_r . kcode_j),   O_r = sum_j p_rj * v_scale_j * vcode_j
+// (the codes take part without being decompressed first: "Flash Attention on Ascend: three
+// techniques", section 3).  The keys each sequence owns go through the paged split kernel of
+// decode.cuh; both write partial outputs with their log-sum-exp, and fa_shared_combine_kernel
+// merges them: L = log sum_s exp(L_s), O = sum_s exp(L_s - L) O_s.
+//
+// fa_shared_prefix_kernel, one CTA per (KV head, block of rows, split of the prefix), 512 threads:
+//   warps 0-3   softmax of S tile 0 (thread = query row = TMEM lane), warps 4-7 of S tile 1
+//   warps 8-11  dequantisation: thread = key; K codes to fp16 (exact), V codes times their scale to
+//               fp16, both into the swizzled layout the tensor core reads
+//   warp 12     TMA producer: K and V code tiles of 128 keys, one box per page piece
+//   warp 13     allocates TMEM and issues tcgen05.mma from one thread: S_t = Q_t K^T,
+//               O_t += P_t V with P_t from TMEM;  warps 14-15 idle
+// The two S tiles are two blocks of 128 query rows that share every K/V tile (kStream = false), or,
+// when R <= 128, two interleaved streams of key tiles over one block of rows (kStream = true), merged
+// in shared memory at the end; either way one tile's softmax runs while the tensor core works on
+// the other.
+//
+// Number formats.  Q is scaled per row by a power of two and kept in fp16, which holds a bf16 row
+// exactly (elements more than 2^29 below the row's largest lose bits).  Scores, maxima, sums, O and
+// log-sum-exps are fp32; k_scale multiplies the fp32 scores, so QK^T has no rounding of its
+// own.  P = 2^7 p (p <= 2^8 with the lazy maximum) and v_scale * vcode * 2^E are rounded to fp16
+// (relative 2^-11 each, an eighth of the bf16 output's): the shift by 2^7 keeps weights down to
+// 2^-31 of the maximum from vanishing, and the power E, lowered (with an exact rescale of O) when a
+// larger v_scale arrives, keeps V below 2^15.
+#pragma once
+
+#include "decode.cuh"
+#include "sm100.cuh"
+
+namespace fa {
+
+struct SharedParams {
+  const uint16_t* q;  // bf16 [B, 1, Hq, D]
+  const float* k_scale;  // [num_pages, Hkv, P]
+  const float* v_scale;
+  const int32_t* table;  // [max_pages] pages of the prefix
+  const int32_t* len;    // [1] keys of the prefix
+  float* o_part;         // [splits, B, Hq, D]
+  float* lse_part;       // [splits, B, Hq] natural log
+  int B, Hq, Hkv, G, R, row_blocks, splits;
+  int max_pages, num_pages, page_shift;
+  float scale_log2;
+  uint64_t timeout_ns;
+};
+
+template <int D, int kBits, bool kStream>
+struct SharedCfg {
+  static constexpr int kThreads = 512;
+  static constexpr int kRow = D * kBits / 8;       // bytes of one row of codes
+  static constexpr int kAtom = 128 * 128;          // 128 rows x 128 bytes (64 fp16)
+  static constexpr int kTile = 128 * D * 2;        // 128 rows of fp16
+  static constexpr int kRawTile = 128 * kRow;
+  static constexpr int kQTiles = kStream ? 1 : 2;
+  // stages of code tiles: as many as fit beside two fp16 stages of K and V
+  static constexpr int kRaw = (kStream || D == 64 || kBits == 4) ? 2 : 1;
+  static constexpr int kQOff = 0;
+  static constexpr int kKOff = kQTiles * kTile;
+  static constexpr int kVOff = kKOff + 2 * kTile;
+  static constexpr int kRawKOff = kVOff + 2 * kTile;
+  static constexpr int kRawVOff = kRawKOff + kRaw * kRawTile;
+  static constexpr int kScaleOff = kRawVOff + kRaw * kRawTile;  // fp32 k_scale [4 tiles][128]
+  static constexpr int kVmaxOff = kScaleOff + 4 * 128 * 4;      // fp32 largest v_scale [4][4 warps]
+  static constexpr int kLseOff = kVmaxOff + 4 * 4 * 4;          // fp32 [128], kStream only
+  static constexpr int kBarOff = kLseOff + (kStream ? 512 : 0);
+  static constexpr int kBarQ = 0;                    // [2]
+  static constexpr int kBarRawKFull = 2;             // [kRaw]
+  static constexpr int kBarRawVFull = kBarRawKFull + kRaw;
+  static constexpr int kBarRawKEmpty = kBarRawVFull + kRaw;
+  static constexpr int kBarRawVEmpty = kBarRawKEmpty + kRaw;
+  static constexpr int kBarKFull = kBarRawVEmpty + kRaw;  // [2]
+  static constexpr int kBarVFull = kBarKFull + 2;
+  static constexpr int kBarKEmpty = kBarVFull + 2;
+  static constexpr int kBarVEmpty = kBarKEmpty + 2;
+  static constexpr int kBarScale = kBarVEmpty + 2;   // [4]
+  static constexpr int kBarSFull = kBarScale + 4;    // [2]
+  static constexpr int kBarPFull = kBarSFull + 2;    // [2 tiles][2 halves]
+  static constexpr int kBarOFinal = kBarPFull + 4;   // [2]
+  static constexpr int kBarDrain = kBarOFinal + 2;
+  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kMiscOff = kBarOff + 8 * kNumBars;
+  static constexpr int kSmemBytes = kMiscOff + 16;
+  static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+  static constexpr uint32_t kTmemCols = 512;
+  __host__ __device__ static constexpr uint32_t colS(int t) { return 128u * t; }
+  __host__ __device__ static constexpr uint32_t colO(int t) { return 256u + uint32_t(D) * t; }
+  // the launch's 512 x 128 registers: two softmax warpgroups, dequantisation, producer + MMA
+  static constexpr uint32_t kRegsSoftmax = 192, kRegsDequant = 72, kRegsOther = 56;
+  static constexpr int kLaunchRegs = 128;
+  static_assert(2 * kRegsSoftmax + kRegsDequant + kRegsOther == 4 * kLaunchRegs, "register split");
+};
+
+// Instruction descriptor for kind::f16 with fp16 A/B and an fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t(N) >> 3) << 17) |
+         ((uint32_t(M) >> 4) << 24);
+}
+
+// Largest exponent e with x * 2^e < 2^top (x >= 0), kept where 2^e and 2^-e are normal fp32 numbers.
+__device__ __forceinline__ int exponent_below(float x, int top) {
+  const int ex = static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 126;  // x < 2^ex
+  return max(-120, min(120, top - ex));
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                       uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
+// One key's row of codes (in the raw tile, swizzled by its TMA box) to fp16 in the layout of a
+// tensor-core operand: 64-dim atoms of 128-byte rows, 16-byte chunk index XOR row % 8.  kScale:
+// values times vs (an fp16 pair).  INT4: within each 8-dim chunk the dims stand in the order 0, 4,
+// 2, 6, 1, 5, 3, 7 (that of the nibble extraction); the last four come out as 16 x the code,
+// which vs_hi = vs / 16 or the other operand undoes.
+template <int D, int kBits, bool kScale>
+__device__ __forceinline__ void dequant_row(uint32_t raw, uint32_t dst, int r, uint32_t vs,
+                                            uint32_t vs_hi) {
+  constexpr int kRow = D * kBits / 8;
+  const uint32_t row = dst + r * 128;
+  auto put = [&](int chunk, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    if constexpr (kScale) {
+      a = mul_f16x2(a, vs);
+      b = mul_f16x2(b, vs);
+      c = mul_f16x2(c, vs_hi);
+      d = mul_f16x2(d, vs_hi);
+    }
+    sts128(row + (chunk >> 3) * (128 * 128) + (((chunk & 7) ^ (r & 7)) << 4), a, b, c, d);
+  };
+#pragma unroll
+  for (int c = 0; c < kRow / 16; ++c) {
+    const uint4 x = lds128(raw + swz<kRow>(r * kRow + 16 * c));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if constexpr (kBits == 8) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t u = w[2 * h] ^ 0x80808080u, v = w[2 * h + 1] ^ 0x80808080u;
+        put(2 * c + h, codes_to_f16x2(u, kSelB01), codes_to_f16x2(u, kSelB23),
+            codes_to_f16x2(v, kSelB01), codes_to_f16x2(v, kSelB23));
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        put(4 * c + h, nib_lo_f16x2(w[h]), nib_lo_f16x2(w[h] >> 8), nib_hi16_f16x2(w[h]),
+            nib_hi16_f16x2(w[h] >> 8));
+    }
+  }
+}
+
+template <int D, int kBits, bool kStream>
+__global__ void __launch_bounds__(512, 1)
+    fa_shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v, const SharedParams p) {
+  using C = SharedCfg<D, kBits, kStream>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // the swizzled tiles need 1024-byte aligned shared memory, and there is no room to align it here
+  if ((smem_u32(smem_raw) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicOr(&g_fa_device_status, kDevStatusLayout);
+    return;
+  }
+  uint8_t* smem = smem_raw;
+  const uint32_t sb = smem_u32(smem);
+  auto bar = [&](int idx) { return sb + C::kBarOff + 8u * idx; };
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+  int* abort_flag = reinterpret_cast<int*>(smem + C::kMiscOff + 4);
+  const WaitCtl ctl{abort_flag, p.timeout_ns};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // KV heads vary fastest, then row blocks: CTAs that run together read the same key rows
+  const int kvh = static_cast<int>(blockIdx.x) % p.Hkv;
+  const int rb = static_cast<int>(blockIdx.x) / p.Hkv % p.row_blocks;
+  const int split = static_cast<int>(blockIdx.x) / (p.Hkv * p.row_blocks);
+  const int row0 = rb * 256;
+  const int live = min(kStream ? 128 : 256, p.R - row0);  // query rows of this CTA
+
+  int len = p.len[0];
+  {
+    const int cap = p.max_pages << p.page_shift;
+    if (len < 0 || len > cap) {
+      if (threadIdx.x == 0) atomicOr(&g_fa_device_status, kDevStatusBadIndex);
+      len = max(0, min(len, cap));
+    }
+  }
+  // splits are whole tiles, as even as they come: the first `extra` splits take one more
+  const int tiles = (len + 127) / 128;
+  const int per = tiles / p.splits, extra = tiles % p.splits;
+  const int t_begin = (split * per + min(split, extra)) * 128;
+  const int nt = per + (split < extra ? 1 : 0);
+  const int t_end = min(len, t_begin + 128 * nt);
+
+  // query row r of this CTA: head kvh * G + (row0 + r) % G of sequence (row0 + r) / G
+  auto out_row = [&](int r) -> size_t {
+    const int x = row0 + r;
+    return static_cast<size_t>(x / p.G) * p.Hq + static_cast<size_t>(kvh) * p.G + x % p.G;
+  };
+  const size_t rows = static_cast<size_t>(p.B) * p.Hq;
+  if (nt == 0) {
+    for (int r = threadIdx.x; r < live; r += blockDim.x)
+      p.lse_part[split * rows + out_row(r)] = -INFINITY;
+    return;
+  }
+  const bool act1 = kStream ? nt > 1 : live > 128;  // S tile 1 has work
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kNumBars; ++i) {
+      uint32_t count = 1;
+      if (i < 2 || (i >= C::kBarPFull && i < C::kBarPFull + 4)) count = 128;
+      if ((i >= C::kBarRawKEmpty && i < C::kBarKEmpty) ||
+          (i >= C::kBarScale && i < C::kBarScale + 4))
+        count = 4;
+      mbar_init(bar(i), count);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12 && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 13) {
+    tmem_alloc(smem_u32(tmem_holder), C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  auto checked_page = [&](int slot) -> int {
+    int pg = p.table[slot];
+    if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.num_pages)) {
+      atomicOr(&g_fa_device_status, kDevStatusBadIndex);
+      pg = 0;
+    }
+    return pg;
+  };
+
+  if (warp >= 12) {
+    setmaxnreg_dec<C::kRegsOther>();
+    if (warp == 12) {
+      // ================= TMA producer =================
+      // lane i < boxes copies box i of each tile (a page, or 128 keys of a larger one); boxes past
+      // the last key are skipped: the codes left there are finite and their scales count as 0
+      const int box_t = min(128, 1 << p.page_shift);
+      const int boxes = 128 / box_t;
+      const int pmask = (1 << p.page_shift) - 1;
+      const uint32_t box_bytes = static_cast<uint32_t>(box_t) * C::kRow;
+      const uint64_t pol = l2_evict_first_policy();
+      auto page_at = [&](int j) -> int {
+        const int t = t_begin + 128 * j + lane * box_t;
+        return lane < boxes && j < nt && t < t_end ? checked_page(t >> p.page_shift) : -1;
+      };
+      int pg = page_at(0), issued = 0;
+      bool ok = true;
+      for (int j = 0; j < nt && ok; ++j) {
+        const int pg_next = page_at(j + 1);
+        const int s = j % C::kRaw, ph = (j / C::kRaw) & 1;
+        const int t = t_begin + 128 * j + lane * box_t;
+        const uint32_t n_live = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+          const uint32_t full = bar((kind ? C::kBarRawVFull : C::kBarRawKFull) + s);
+          ok = ok && mbar_wait(bar((kind ? C::kBarRawVEmpty : C::kBarRawKEmpty) + s), ph ^ 1, ctl);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(full, n_live * box_bytes);
+          __syncwarp();
+          const uint32_t dst = sb + (kind ? C::kRawVOff : C::kRawKOff) + s * C::kRawTile +
+                               lane * box_t * C::kRow;
+          if (pg >= 0) {
+            // several row blocks read the prefix: let it stay in L2 for them
+            if (p.row_blocks > 1)
+              tma_load_4d(dst, kind ? &tm_v : &tm_k, full, 0, kvh, t & pmask, pg);
+            else
+              tma_load_4d_policy(dst, kind ? &tm_v : &tm_k, full, 0, kvh, t & pmask, pg, pol);
+          }
+          issued = 2 * j + kind + 1;
+        }
+        pg = pg_next;
+      }
+      // Every copy this warp started has landed before the CTA can exit (already true unless a
+      // consumer gave up; then this waits, bounded).
+      __syncwarp();
+      if (lane == 0) {
+        volatile int zero = 0;
+        const WaitCtl drain_ctl{&zero, p.timeout_ns};
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+          const int n = (issued + 1 - kind) / 2;  // tiles of this kind
+          for (int s = 0; s < C::kRaw && s < n; ++s)
+            mbar_wait(bar((kind ? C::kBarRawVFull : C::kBarRawKFull) + s),
+                      ((n - 1 - s) / C::kRaw) & 1, drain_ctl);
+        }
+      }
+    } else if (warp == 13 && lane == 0) {
+      // ================= MMA issuer =================
+      constexpr uint32_t idesc_qk = idesc_f16_f32(128, 128, false);
+      constexpr uint32_t idesc_pv = idesc_f16_f32(128, D, true);
+      auto issue_qk = [&](int t, int slot) {
+        const uint32_t qa = sb + C::kQOff + (kStream ? 0 : t) * C::kTile;
+        const uint32_t kb = sb + C::kKOff + slot * C::kTile;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * C::kAtom + (kk % 4) * 32;
+          umma_ss(tmem + C::colS(t), smem_desc_sw128(qa + off, 16, 1024),
+                  smem_desc_sw128(kb + off, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(bar(C::kBarSFull + t));
+      };
+      // O_t += P_t V; P_t arrives in two halves of 64 keys
+      auto issue_pv = [&](int t, int slot, bool first, int phase) -> bool {
+        const uint32_t vb = sb + C::kVOff + slot * C::kTile;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!mbar_wait(bar(C::kBarPFull + 2 * t + half), phase, ctl)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4) {
+            const int kk = 4 * half + k4;
+            umma_ts(tmem + C::colO(t), tmem + C::colS(t) + kk * 8,
+                    smem_desc_sw128(vb + kk * 16 * 128, C::kAtom, 1024), idesc_pv,
+                    (first && kk == 0) ? 0u : 1u);
+          }
+        }
+        return true;
+      };
+      // tile j sits in slot j & 1 of K and V, in that slot's use number j >> 1
+      auto k_wait = [&](int j) {
+        return mbar_wait(bar(C::kBarKFull + (j & 1)), (j >> 1) & 1, ctl);
+      };
+      auto v_wait = [&](int j) {
+        return mbar_wait(bar(C::kBarVFull + (j & 1)), (j >> 1) & 1, ctl);
+      };
+      bool ok = mbar_wait(bar(C::kBarQ), 0, ctl);
+      if (!kStream && ok && act1) ok = mbar_wait(bar(C::kBarQ + 1), 0, ctl);
+      if constexpr (kStream) {
+        for (int j = 0; j < min(2, nt) && ok; ++j) {
+          if (!(ok = k_wait(j))) break;
+          tc_fence_after();
+          issue_qk(j, j);
+          tc_commit(bar(C::kBarKEmpty + j));
+        }
+        for (int j = 0; j < nt && ok; ++j) {
+          const int t = j & 1;
+          if (!(ok = v_wait(j))) break;
+          if (!(ok = issue_pv(t, t, j < 2, (j >> 1) & 1))) break;
+          tc_commit(bar(C::kBarVEmpty + t));
+          if (j + 2 < nt) {
+            if (!(ok = k_wait(j + 2))) break;
+            tc_fence_after();
+            issue_qk(t, t);
+            tc_commit(bar(C::kBarKEmpty + t));
+          } else {
+            tc_commit(bar(C::kBarOFinal + t));
+          }
+        }
+      } else if (ok && (ok = k_wait(0))) {
+        tc_fence_after();
+        issue_qk(0, 0);
+        if (act1) issue_qk(1, 0);
+        tc_commit(bar(C::kBarKEmpty + 0));
+        for (int j = 0; j < nt; ++j) {
+          const int slot = j & 1;
+          const bool next = j + 1 < nt;
+          if (!v_wait(j)) break;
+          if (!issue_pv(0, slot, j == 0, j & 1)) break;
+          if (next) {
+            if (!k_wait(j + 1)) break;
+            tc_fence_after();
+            issue_qk(0, slot ^ 1);
+          } else {
+            tc_commit(bar(C::kBarOFinal + 0));
+          }
+          if (act1) {
+            if (!issue_pv(1, slot, j == 0, j & 1)) break;
+            if (!next) tc_commit(bar(C::kBarOFinal + 1));
+          }
+          tc_commit(bar(C::kBarVEmpty + slot));
+          if (next) {
+            if (act1) issue_qk(1, slot ^ 1);
+            tc_commit(bar(C::kBarKEmpty + (slot ^ 1)));
+          }
+        }
+      }
+      // Drain: every MMA this thread issued has completed before TMEM is released.
+      tc_commit(bar(C::kBarDrain));
+      volatile int zero = 0;
+      const WaitCtl drain_ctl{&zero, p.timeout_ns};
+      mbar_wait(bar(C::kBarDrain), 0, drain_ctl);
+    }
+  } else if (warp >= 8) {
+    setmaxnreg_dec<C::kRegsDequant>();
+    // ================= dequantisation: thread r = key r of each tile =================
+    const int r = threadIdx.x & 127, w4 = warp & 3;
+    const int pmask = (1 << p.page_shift) - 1;
+    // page of this thread's key of tile j (-1: past the prefix), two tiles ahead; scales one ahead
+    auto page_at = [&](int j) -> int {
+      const int t = t_begin + 128 * j + r;
+      return j < nt && t < t_end ? checked_page(t >> p.page_shift) : -1;
+    };
+    auto scale_at = [&](const float* s, int j, int pg) -> float {
+      if (pg < 0) return 0.f;
+      const int t = t_begin + 128 * j + r;
+      return __ldg(s + (((static_cast<size_t>(pg) * p.Hkv + kvh) << p.page_shift) + (t & pmask)));
+    };
+    int pg = page_at(0);
+    float ks = scale_at(p.k_scale, 0, pg), vs = scale_at(p.v_scale, 0, pg);
+    pg = page_at(1);
+    constexpr int kUnset = 1 << 20;
+    int E[2] = {kUnset, kUnset};  // of the accumulators the tile goes to
+    for (int j = 0; j < nt; ++j) {
+      const float ks_next = scale_at(p.k_scale, j + 1, pg), vs_next = scale_at(p.v_scale, j + 1, pg);
+      pg = page_at(j + 2);
+      const int s = j % C::kRaw, ph = (j / C::kRaw) & 1, slot = j & 1;
+      // --- K: the slot's last reader is done, so is everyone with this entry of the scale ring ---
+      bool ok = mbar_wait(bar(C::kBarKEmpty + slot), ((j >> 1) & 1) ^ 1, ctl);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      float* ring = reinterpret_cast<float*>(smem + C::kScaleOff) + (j & 3) * 128;
+      float* vmax = reinterpret_cast<float*>(smem + C::kVmaxOff) + (j & 3) * 4;
+      ring[r] = ks;
+      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(vs)));
+      if (lane == 0) vmax[w4] = __uint_as_float(top);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::kBarScale + (j & 3)));
+      ok = mbar_wait(bar(C::kBarRawKFull + s), ph, ctl);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      dequant_row<D, kBits, false>(sb + C::kRawKOff + s * C::kRawTile,
+                                   sb + C::kKOff + slot * C::kTile, r, 0u, 0u);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(C::kBarRawKEmpty + s));
+        mbar_arrive(bar(C::kBarKFull + slot));
+      }
+      // --- V: times v_scale * 2^E ---
+      ok = mbar_wait(bar(C::kBarScale + (j & 3)), (j >> 2) & 1, ctl) &&
+           mbar_wait(bar(C::kBarRawVFull + s), ph, ctl) &&
+           mbar_wait(bar(C::kBarVEmpty + slot), ((j >> 1) & 1) ^ 1, ctl);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const float4 vm = *reinterpret_cast<const float4*>(vmax);
+      int& e = E[kStream ? slot : 0];
+      e = min(e, exponent_below(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)), 8));
+      const float vsx = vs * exp2i(e);
+      dequant_row<D, kBits, true>(sb + C::kRawVOff + s * C::kRawTile,
+                                  sb + C::kVOff + slot * C::kTile, r, pack_f16x2(vsx, vsx),
+                                  kBits == 4 ? pack_f16x2(vsx * 0.0625f, vsx * 0.0625f)
+                                             : pack_f16x2(vsx, vsx));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(C::kBarRawVEmpty + s));
+        mbar_arrive(bar(C::kBarVFull + slot));
+      }
+      ks = ks_next;
+      vs = vs_next;
+    }
+  } else {
+    setmaxnreg_inc<C::kRegsSoftmax>();
+    // ================= Q, softmax, epilogue: thread r = query row r of S tile t =================
+    const int t = warp >> 2;
+    const int r = threadIdx.x & 127;
+    const int R = (kStream ? 0 : t * 128) + r;  // row of the CTA
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint32_t colS = t ? C::colS(1) : C::colS(0);
+    const uint32_t colO = t ? C::colO(1) : C::colO(0);
+    const bool warp_live = (R & ~31) < live;  // a warp of padding rows only keeps the barriers
+    const int first = kStream ? t : 0, step = kStream ? 2 : 1;
+
+    float sc = 0.f;  // score units: log2, undoing the row's power of two
+    {
+      uint4 x[D / 8];
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + out_row(min(R, live - 1)) * D);
+      uint32_t am = 0;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        x[c] = R < live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        const uint32_t kAbs = 0x7fff7fffu;
+        am = __vmaxu2(am, __vmaxu2(__vmaxu2(x[c].x & kAbs, x[c].y & kAbs),
+                                   __vmaxu2(x[c].z & kAbs, x[c].w & kAbs)));
+      }
+      const int eq = exponent_below(__uint_as_float(max(am & 0xffffu, am >> 16) << 16), 15);
+      const float qs = exp2i(eq);
+      // (not 0: a masked score is -infinity times this)
+      sc = fmaxf(p.scale_log2 * exp2i(-eq), 0x1p-126f);
+      if (!kStream || t == 0) {
+        const uint32_t row = sb + C::kQOff + (kStream ? 0 : t) * C::kTile + r * 128;
+        // INT4: the K operand's dim order, and 1/16 for its 16 x codes
+        const float qh = kBits == 4 ? qs * 0.0625f : qs;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+          }
+          uint32_t h[4];
+          if constexpr (kBits == 8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = pack_f16x2(f[2 * i] * qs, f[2 * i + 1] * qs);
+          } else {
+            h[0] = pack_f16x2(f[0] * qs, f[4] * qs);
+            h[1] = pack_f16x2(f[2] * qs, f[6] * qs);
+            h[2] = pack_f16x2(f[1] * qh, f[5] * qh);
+            h[3] = pack_f16x2(f[3] * qh, f[7] * qh);
+          }
+          sts128(row + (c >> 3) * C::kAtom + (((c & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(C::kBarQ + t));
+      }
+    }
+
+    float m = -INFINITY, l = 0.f;
+    constexpr int kUnset = 1 << 20;
+    int E = kUnset, n = 0;
+    for (int j = first; j < (t == 0 || act1 ? nt : 0); j += step, ++n) {
+      bool ok = mbar_wait(bar(C::kBarSFull + t), n & 1, ctl);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      if (!warp_live) {  // whatever P holds for padding rows stays in those rows
+        mbar_arrive(bar(C::kBarPFull + 2 * t));
+        mbar_arrive(bar(C::kBarPFull + 2 * t + 1));
+        continue;
+      }
+      uint32_t sv[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(trow + colS + 32 * c, sv[c]);
+      ok = mbar_wait(bar(C::kBarScale + (j & 3)), (j >> 2) & 1, ctl);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tmem_wait_ld();
+      // raw scores times k_scale (the row's common factor sc joins in the exponent)
+      const uint32_t ring = sb + C::kScaleOff + (j & 3) * 512;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int q4 = 0; q4 < 8; ++q4) {
+          const uint4 k4 = lds128(ring + 128 * c + 16 * q4);
+          const uint64_t a = f2_mul(f2(__uint_as_float(sv[c][4 * q4]), __uint_as_float(sv[c][4 * q4 + 1])),
+                                    f2(__uint_as_float(k4.x), __uint_as_float(k4.y)));
+          const uint64_t b = f2_mul(f2(__uint_as_float(sv[c][4 * q4 + 2]), __uint_as_float(sv[c][4 * q4 + 3])),
+                                    f2(__uint_as_float(k4.z), __uint_as_float(k4.w)));
+          float a0, a1, b0, b1;
+          f2_split(a, a0, a1);
+          f2_split(b, b0, b1);
+          sv[c][4 * q4] = __float_as_uint(a0);
+          sv[c][4 * q4 + 1] = __float_as_uint(a1);
+          sv[c][4 * q4 + 2] = __float_as_uint(b0);
+          sv[c][4 * q4 + 3] = __float_as_uint(b1);
+        }
+      const int limit = t_end - (t_begin + 128 * j);
+      if (limit < 128) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (32 * c + k >= limit) sv[c][k] = __float_as_uint(-INFINITY);
+      }
+      float mx[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) mx[c] = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int col = 16 * i + 2 * c;
+          mx[c] = fmax3(mx[c], __uint_as_float(sv[col / 32][col % 32]),
+                        __uint_as_float(sv[(col + 1) / 32][(col + 1) % 32]));
+        }
+      const float m_new = fmaxf(m, fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
+                                         fmaxf(mx[6], mx[7])) * sc);
+      const float4 vm = *reinterpret_cast<const float4*>(smem + C::kVmaxOff + (j & 3) * 16);
+      const int e_new =
+          min(E, exponent_below(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)), 8));
+      // O is rescaled when the maximum grew by more than 2^8 (until then the old one stays the
+      // reference and p may reach 2^8) or V's exponent fell
+      float alpha = 1.f;
+      bool resc = false;
+      if (n == 0) {
+        m = m_new;
+      } else {
+        if (m_new > m + 8.f) {
+          resc = true;
+          alpha = ex2(m - m_new);
+          m = m_new;
+        }
+        resc = resc || e_new != E;
+      }
+      if (__any_sync(0xffffffffu, resc)) {
+        const float a = alpha * exp2i_or_zero(e_new - E);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(trow + colO + 32 * c, ov);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * a);
+          tmem_st32(trow + colO + 32 * c, ov);
+        }
+      }
+      E = e_new;
+      // p = 2^(x * sc - m + 7) as fp16 pairs over S's columns, one half of the keys at a time
+      const float shift = (m == -INFINITY) ? 0.f : 7.f - m;
+      const uint64_t sc2 = f2(sc, sc), shift2 = f2(shift, shift);
+      uint64_t acc0 = f2(0.f, 0.f), acc1 = f2(0.f, 0.f);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int col = 64 * half + 2 * k;
+          const uint64_t x = f2_fma(f2(__uint_as_float(sv[col / 32][col % 32]),
+                                       __uint_as_float(sv[(col + 1) / 32][(col + 1) % 32])),
+                                    sc2, shift2);
+          float x0, x1;
+          f2_split(x, x0, x1);
+          const float a = ex2(x0), b = ex2(x1);
+          if (k & 1) acc1 = f2_add(acc1, f2(a, b)); else acc0 = f2_add(acc0, f2(a, b));
+          pk[k] = pack_f16x2(a, b);
+        }
+        tmem_st32(trow + colS + 32 * half, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(C::kBarPFull + 2 * t + half));
+      }
+      float a0, a1, a2, a3;
+      f2_split(acc0, a0, a1);
+      f2_split(acc1, a2, a3);
+      l = l * alpha + ((a0 + a1) + (a2 + a3));
+    }
+
+    // ---- partial output O / l * 2^-E and log-sum-exp (log2 units; l carries 2^7) ----
+    bool have = false;
+    if (n > 0) {
+      const bool ok = mbar_wait(bar(C::kBarOFinal + t), 0, ctl);
+      have = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    const bool some = have && warp_live && l != 0.f;
+    const float inv_l = some ? 1.f / l : 0.f;
+    const float unscale = E == kUnset ? 0.f : exp2i(-E);
+    float lse2 = some ? m + (log2f(l) - 7.f) : -INFINITY;
+    float w0 = 1.f, w1 = 0.f;
+    float* lse_x = reinterpret_cast<float*>(smem + C::kLseOff);
+    // stream 1 leaves its normalised rows in the K and V slots that only it used (every product
+    // of its tiles has completed), D / 2 dims in each, 16-byte pieces XORed with the row
+    auto x_addr = [&](int d) {  // of dims d .. d + 3
+      constexpr int kHalf = D / 2;
+      const int q = (d % kHalf) / 4;
+      return sb + (d < kHalf ? C::kKOff : C::kVOff) + C::kTile + r * (kHalf * 4) +
+             ((q ^ (r & 7)) << 4);
+    };
+    if constexpr (kStream) {
+      if (t == 1) lse_x[r] = lse2;
+      if (t == 0) {
+        named_bar_sync(1, 256);
+        const float other = lse_x[r];
+        const float top = fmaxf(lse2, other);
+        w0 = lse2 == -INFINITY ? 0.f : ex2(lse2 - top);
+        w1 = other == -INFINITY ? 0.f : ex2(other - top);
+        const float sum = w0 + w1;
+        lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        w0 *= inv;
+        w1 *= inv;
+      }
+    }
+    const size_t orow = out_row(min(R, live - 1));
+    float* dst = p.o_part + (split * rows + orow) * D;
+    if (warp_live) {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t ov[32];
+        if (have) {
+          tmem_ld32(trow + colO + 32 * c, ov);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int q8 = 0; q8 < 4; ++q8) {
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            // INT4: column i of a chunk holds dim 0, 4, 2, 6, 1, 5, 3, 7
+            const int dim = kBits == 4 ? ((i & 1) << 2 | (i & 2) | (i >> 2)) : i;
+            f[dim] = some ? __uint_as_float(ov[8 * q8 + i]) * inv_l * unscale : 0.f;
+          }
+          const int d = 32 * c + 8 * q8;
+          if (kStream && t == 1) {
+            sts128(x_addr(d), __float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                   __float_as_uint(f[3]));
+            sts128(x_addr(d + 4), __float_as_uint(f[4]), __float_as_uint(f[5]),
+                   __float_as_uint(f[6]), __float_as_uint(f[7]));
+          } else {
+            if constexpr (kStream) {
+              if (act1) {
+                const uint4 y0 = lds128(x_addr(d)), y1 = lds128(x_addr(d + 4));
+                const uint32_t y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = w0 * f[i] + w1 * __uint_as_float(y[i]);
+              }
+            }
+            if (R < live) {
+              *reinterpret_cast<float4*>(dst + d) = make_float4(f[0], f[1], f[2], f[3]);
+              *reinterpret_cast<float4*>(dst + d + 4) = make_float4(f[4], f[5], f[6], f[7]);
+            }
+          }
+        }
+      }
+    }
+    if (kStream && t == 1) named_bar_sync(1, 256);
+    if ((!kStream || t == 0) && R < live)
+      p.lse_part[split * rows + orow] = lse2 * 0.69314718055994531f;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// One warp per (sequence, query head): merges `splits` partials (those of the sequence's own keys,
+// then those of the prefix).  A partial with log-sum-exp -inf holds no key and is not read.
+template <int D>
+__global__ void __launch_bounds__(128) fa_shared_combine_kernel(const CombineParams p) {
+  constexpr int V = D / 32;  // dims per lane
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int rows = p.B * p.Hq;
+  if (row >= rows) return;
+  float top = -INFINITY;
+  for (int s = lane; s < p.splits; s += 32)
+    top = fmaxf(top, p.lse_part[static_cast<size_t>(s) * rows + row]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float sum = 0.f, acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const size_t at = static_cast<size_t>(s) * rows + row;
+    const float ls = p.lse_part[at];
+    if (ls == -INFINITY) continue;
+    const float w = expf(ls - top);
+    sum += w;
+    const float* src = p.o_part + at * D + V * lane;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] += w * src[i];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint16_t* dst = p.o + static_cast<size_t>(row) * D + V * lane;
+#pragma unroll
+  for (int i = 0; i < V; i += 2)
+    *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+  if (lane == 0 && p.lse != nullptr) p.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
+}
+
+}  // namespace fa
