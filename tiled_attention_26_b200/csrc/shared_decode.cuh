@@ -140,10 +140,12 @@ __device__ __forceinline__ void dequant_row(uint32_t raw, uint32_t dst, int r, u
     }
     sts128(row + (chunk >> 3) * (128 * 128) + (((chunk & 7) ^ (r & 7)) << 4), a, b, c, d);
   };
+  uint4 x[kRow / 16];  // the whole row first: the loads' latency is paid once
+#pragma unroll
+  for (int c = 0; c < kRow / 16; ++c) x[c] = lds128(raw + swz<kRow>(r * kRow + 16 * c));
 #pragma unroll
   for (int c = 0; c < kRow / 16; ++c) {
-    const uint4 x = lds128(raw + swz<kRow>(r * kRow + 16 * c));
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
     if constexpr (kBits == 8) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -309,20 +311,23 @@ __global__ void __launch_bounds__(512, 1)
       // ================= MMA issuer =================
       constexpr uint32_t idesc_qk = idesc_f16_f32(128, 128, false);
       constexpr uint32_t idesc_pv = idesc_f16_f32(128, D, true);
+      // operand descriptors differ in the address field only (16-byte units, low word): one add each
+      const uint64_t desc_k_major = smem_desc_sw128(0, 16, 1024);
+      const uint64_t desc_v = smem_desc_sw128(0, C::kAtom, 1024);
       auto issue_qk = [&](int t, int slot) {
-        const uint32_t qa = sb + C::kQOff + (kStream ? 0 : t) * C::kTile;
-        const uint32_t kb = sb + C::kKOff + slot * C::kTile;
+        const uint32_t qa = (sb + C::kQOff + (kStream ? 0 : t) * C::kTile) >> 4;
+        const uint32_t kb = (sb + C::kKOff + slot * C::kTile) >> 4;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * C::kAtom + (kk % 4) * 32;
-          umma_ss(tmem + C::colS(t), smem_desc_sw128(qa + off, 16, 1024),
-                  smem_desc_sw128(kb + off, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
+          const uint32_t off = ((kk / 4) * C::kAtom + (kk % 4) * 32) >> 4;
+          umma_ss(tmem + C::colS(t), desc_k_major + (qa + off), desc_k_major + (kb + off), idesc_qk,
+                  kk > 0 ? 1u : 0u);
         }
         tc_commit(bar(C::kBarSFull + t));
       };
       // O_t += P_t V; P_t arrives in two halves of 64 keys
       auto issue_pv = [&](int t, int slot, bool first, int phase) -> bool {
-        const uint32_t vb = sb + C::kVOff + slot * C::kTile;
+        const uint32_t vb = (sb + C::kVOff + slot * C::kTile) >> 4;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (!mbar_wait(bar(C::kBarPFull + 2 * t + half), phase, ctl)) return false;
@@ -330,8 +335,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {
             const int kk = 4 * half + k4;
-            umma_ts(tmem + C::colO(t), tmem + C::colS(t) + kk * 8,
-                    smem_desc_sw128(vb + kk * 16 * 128, C::kAtom, 1024), idesc_pv,
+            umma_ts(tmem + C::colO(t), tmem + C::colS(t) + kk * 8, desc_v + (vb + kk * 128), idesc_pv,
                     (first && kk == 0) ? 0u : 1u);
           }
         }
@@ -372,26 +376,23 @@ __global__ void __launch_bounds__(512, 1)
         issue_qk(0, 0);
         if (act1) issue_qk(1, 0);
         tc_commit(bar(C::kBarKEmpty + 0));
-        for (int j = 0; j < nt; ++j) {
+        const int last = act1 ? 1 : 0;
+        for (int j = 0; j < nt && ok; ++j) {
           const int slot = j & 1;
           const bool next = j + 1 < nt;
-          if (!v_wait(j)) break;
-          if (!issue_pv(0, slot, j == 0, j & 1)) break;
-          if (next) {
-            if (!k_wait(j + 1)) break;
-            tc_fence_after();
-            issue_qk(0, slot ^ 1);
-          } else {
-            tc_commit(bar(C::kBarOFinal + 0));
-          }
-          if (act1) {
-            if (!issue_pv(1, slot, j == 0, j & 1)) break;
-            if (!next) tc_commit(bar(C::kBarOFinal + 1));
-          }
-          tc_commit(bar(C::kBarVEmpty + slot));
-          if (next) {
-            if (act1) issue_qk(1, slot ^ 1);
-            tc_commit(bar(C::kBarKEmpty + (slot ^ 1)));
+          if (!(ok = v_wait(j))) break;
+#pragma unroll 1  // (one copy of the issue code: two took more than this warp's registers)
+          for (int t = 0; t <= last; ++t) {
+            if (!(ok = issue_pv(t, slot, j == 0, j & 1))) break;
+            if (t == last) tc_commit(bar(C::kBarVEmpty + slot));
+            if (next) {
+              if (t == 0 && !(ok = k_wait(j + 1))) break;
+              tc_fence_after();
+              issue_qk(t, slot ^ 1);
+              if (t == last) tc_commit(bar(C::kBarKEmpty + (slot ^ 1)));
+            } else {
+              tc_commit(bar(C::kBarOFinal + t));
+            }
           }
         }
       }
@@ -618,13 +619,12 @@ __global__ void __launch_bounds__(512, 1)
       const uint64_t sc2 = f2(sc, sc), shift2 = f2(shift, shift);
       uint64_t acc0 = f2(0.f, 0.f), acc1 = f2(0.f, 0.f);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t pk[32];
+      for (int piece = 0; piece < 4; ++piece) {  // 32 keys
+        uint32_t pk[16];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int col = 64 * half + 2 * k;
-          const uint64_t x = f2_fma(f2(__uint_as_float(sv[col / 32][col % 32]),
-                                       __uint_as_float(sv[(col + 1) / 32][(col + 1) % 32])),
+        for (int k = 0; k < 16; ++k) {
+          const uint64_t x = f2_fma(f2(__uint_as_float(sv[piece][2 * k]),
+                                       __uint_as_float(sv[piece][2 * k + 1])),
                                     sc2, shift2);
           float x0, x1;
           f2_split(x, x0, x1);
@@ -632,10 +632,12 @@ __global__ void __launch_bounds__(512, 1)
           if (k & 1) acc1 = f2_add(acc1, f2(a, b)); else acc0 = f2_add(acc0, f2(a, b));
           pk[k] = pack_f16x2(a, b);
         }
-        tmem_st32(trow + colS + 32 * half, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(C::kBarPFull + 2 * t + half));
+        tmem_st16(trow + colS + 16 * piece, pk);
+        if (piece & 1) {
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(C::kBarPFull + 2 * t + (piece >> 1)));
+        }
       }
       float a0, a1, a2, a3;
       f2_split(acc0, a0, a1);
