@@ -107,11 +107,17 @@ def fa_status_string(status: int) -> str:
 def _stream_ptr(stream):
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        # (the pointer alone: building a Stream object costs several microseconds a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(t, name, dtype, shape, device):
+    try:  # (tens of checks a step: the usual case without building a message or a tuple)
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")

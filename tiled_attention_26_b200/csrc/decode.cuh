@@ -65,6 +65,11 @@ struct DecodeParams {
   const int32_t* block_table;  // [B, max_pages]
   const int32_t* seqlens;      // [B]
   int max_pages, num_pages, page_shift;  // P = 1 << page_shift
+  // Query rows: row i of KV head kvh of sequence b is head kvh * Gq + i % Gq of sequence b + i / Gq
+  // of the tensors (G = Gq, i < G: the sequence's own heads).  A prefix that B sequences share is one
+  // sequence here, of G = B * Gq rows.
+  int Gq;
+  long long rows;  // query rows of the tensors: sequences * Hq
 };
 
 struct CombineParams {
@@ -293,6 +298,13 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
     }
   }
   const int head0 = kvh * p.G + hb * 8;
+  // first element row of q and o_part of the CTA's query row i
+  auto row_of = [&](int i) -> size_t {
+    if constexpr (kPaged)
+      return static_cast<size_t>(b + (hb * 8 + i) / p.Gq) * p.Hq + kvh * p.Gq + (hb * 8 + i) % p.Gq;
+    else
+      return static_cast<size_t>(b) * p.Hq + head0 + i;
+  };
   const int nheads = min(8, p.G - hb * 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -457,7 +469,7 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
   {
     float qv[KS][4];
     const bool hv = g < nheads;
-    const uint16_t* qrow = p.q + (static_cast<size_t>(b) * p.Hq + head0 + (hv ? g : 0)) * D;
+    const uint16_t* qrow = p.q + row_of(hv ? g : 0) * D;
     float amax = 0.f;
 #pragma unroll
     for (int s = 0; s < KS; ++s)
@@ -679,6 +691,10 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
     if (lane == 0) mbar_arrive(bar_empty(s));
   }
 
+  // Where this grid was launched as a programmatic dependent, it does not end before the grid it
+  // depends on: whoever waits for this one then waits for both.
+  if constexpr (kPaged) asm volatile("griddepcontrol.wait;" ::: "memory");
+
   // ---- merge the 4 warps (the stage tiles are free now: every stage has been consumed) ----
   named_bar_sync(1, 128);
   float* sm_o = reinterpret_cast<float*>(smem + C::kMergeO);
@@ -722,7 +738,7 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
       L += f * sm_l[w * 8 + h];
       acc += f * sm_o[(w * 8 + h) * D + d];
     }
-    const size_t row = (static_cast<size_t>(split) * p.B + b) * p.Hq + head0 + h;
+    const size_t row = static_cast<size_t>(split) * p.rows + row_of(h);
     p.o_part[row * D + d] = (L == 0.f) ? 0.f : acc / L;
     if (d == 0) p.lse_part[row] = (L == 0.f) ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
   }
@@ -750,29 +766,33 @@ __global__ void __launch_bounds__(128) fa_decode_combine_kernel(const CombinePar
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  for (int s = lane; s < p.splits; s += 32) {
-    const float ls = p.lse_part[s * stride + row];
-    L += (ls == -INFINITY) ? 0.f : expf(ls - M);
+  // lane i weighs split s0 + i; a split with log-sum-exp -inf holds no key and is not read
+  for (int s0 = 0; s0 < p.splits; s0 += 32) {
+    const float ls = s0 + lane < p.splits ? p.lse_part[(s0 + lane) * stride + row] : -INFINITY;
+    const float mine = (ls == -INFINITY) ? 0.f : expf(ls - M);
+    L += mine;
+    const uint32_t some = __ballot_sync(0xffffffffu, ls != -INFINITY);
+    const int n = min(32, p.splits - s0);
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) {
+      const float w = __shfl_sync(0xffffffffu, mine, s);
+      const bool read = some >> s & 1;
+      const float* src = p.o_part + ((s0 + s) * stride + row) * D + V * lane;
+      if constexpr (V == 4) {
+        const float4 x = read ? *reinterpret_cast<const float4*>(src) : make_float4(0, 0, 0, 0);
+        acc[0] += w * x.x;
+        acc[1 % V] += w * x.y;
+        acc[2 % V] += w * x.z;
+        acc[3 % V] += w * x.w;
+      } else {
+        const float2 x = read ? *reinterpret_cast<const float2*>(src) : make_float2(0, 0);
+        acc[0] += w * x.x;
+        acc[1 % V] += w * x.y;
+      }
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-#pragma unroll 4
-  for (int s = 0; s < p.splits; ++s) {
-    const float ls = p.lse_part[s * stride + row];
-    const float w = (ls == -INFINITY) ? 0.f : expf(ls - M);
-    const float* src = p.o_part + (s * stride + row) * D + V * lane;
-    if constexpr (V == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(src);
-      acc[0] += w * x.x;
-      acc[1 % V] += w * x.y;
-      acc[2 % V] += w * x.z;
-      acc[3 % V] += w * x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(src);
-      acc[0] += w * x.x;
-      acc[1 % V] += w * x.y;
-    }
-  }
   const float inv = (L == 0.f) ? 0.f : 1.f / L;
   uint16_t* dst = p.o + static_cast<size_t>(row) * D + V * lane;
   if constexpr (V == 4) {

@@ -302,40 +302,64 @@ fa::DecodeParams decode_params(const void* q, const int8_t* k, const int8_t* v, 
   p.G = Hq / Hkv;
   p.splits = splits;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.Gq = p.G;
+  p.rows = static_cast<long long>(B) * Hq;
   return p;
 }
 
 std::atomic<uint64_t> g_attr_decode[8];
 
-// Split kernel over grid (Hkv, splits, B * head blocks).  `keys` is the extent of the key axis of
-// the code tensors (Skv, or the page size), `outer` that of the last axis (B, or the number of
-// pages).
-template <int D, bool kPaged, int kBits>
-int launch_split(const fa::DecodeParams& p, int keys, int outer, cudaStream_t stream) {
-  using C = fa::DecodeCfg<D, kBits>;
-  const long long gz = static_cast<long long>(p.B) * ((p.G + 7) / 8);
-  if (p.splits > 65535 || gz > 65535) return FA_ERR_INVALID_ARG;
-  CUtensorMap tk, tv;
-  // a box is one stage (128 keys; past the end of the key axis TMA fills zeros and still counts
-  // the bytes) or, for pages smaller than a stage, one page
-  const uint32_t box = static_cast<uint32_t>(kPaged ? std::min(C::kT, keys) : C::kT);
-  int rc;
-  if ((rc = encode_u8_4d(&tk, p.k, C::kRow, p.Hkv, keys, outer, box)) != FA_OK) return rc;
-  if ((rc = encode_u8_4d(&tv, p.v, C::kRow, p.Hkv, keys, outer, box)) != FA_OK) return rc;
-  auto kernel = fa::fa_decode_split_kernel<D, kPaged, kBits>;
-  const int variant = (D == 128 ? 4 : 0) + (kPaged ? 2 : 0) + (kBits == 4 ? 1 : 0);
-  if ((rc = ensure_smem_attr(kernel, C::kSmemBytes, g_attr_decode[variant])) != FA_OK) return rc;
-  dim3 grid(p.Hkv, p.splits, static_cast<unsigned>(gz));
-  kernel<<<grid, 160, C::kSmemBytes, stream>>>(tk, tv, p);
+// Launches `kernel`; `dependent`: as a programmatic dependent of the launch before it on the stream.
+// Its CTAs may then be scheduled while that one drains (once all of its CTAs have said
+// griddepcontrol.launch_dependents or ended), and order themselves with griddepcontrol.wait.
+template <class... Params, class... Args>
+int launch(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, bool dependent,
+           cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return FA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-// The split kernel, then the merge kernel.
+// K and V codes as the decode kernels' tensor maps: a box is one stage (128 keys; past the end of
+// the key axis TMA fills zeros and still counts the bytes) or, for pages smaller than a stage, one page.
+struct CodeMaps {
+  CUtensorMap k, v;
+};
+int encode_codes(CodeMaps* m, const void* k, const void* v, int row_bytes, int Hkv, int keys,
+                 int outer, bool paged) {
+  const uint32_t box = static_cast<uint32_t>(paged ? std::min(128, keys) : 128);
+  const int rc = encode_u8_4d(&m->k, k, row_bytes, Hkv, keys, outer, box);
+  return rc != FA_OK ? rc : encode_u8_4d(&m->v, v, row_bytes, Hkv, keys, outer, box);
+}
+
+// Split kernel over grid (Hkv, splits, B * head blocks).
 template <int D, bool kPaged, int kBits>
-int launch_split_and_combine(const fa::DecodeParams& p, int keys, int outer, void* o, float* lse,
-                             cudaStream_t stream) {
-  const int rc = launch_split<D, kPaged, kBits>(p, keys, outer, stream);
+int launch_split(const CodeMaps& maps, const fa::DecodeParams& p, bool dependent,
+                 cudaStream_t stream) {
+  using C = fa::DecodeCfg<D, kBits>;
+  static_assert(C::kT == 128, "box of a stage");
+  const long long gz = static_cast<long long>(p.B) * ((p.G + 7) / 8);
+  if (p.splits > 65535 || gz > 65535) return FA_ERR_INVALID_ARG;
+  auto kernel = fa::fa_decode_split_kernel<D, kPaged, kBits>;
+  constexpr int variant = (D == 128 ? 4 : 0) + (kPaged ? 2 : 0) + (kBits == 4 ? 1 : 0);
+  const int rc = ensure_smem_attr(kernel, C::kSmemBytes, g_attr_decode[variant]);
   if (rc != FA_OK) return rc;
+  return launch(kernel, dim3(p.Hkv, p.splits, static_cast<unsigned>(gz)), 160, C::kSmemBytes,
+                dependent, stream, maps.k, maps.v, p);
+}
+
+// Merge of `splits` partials: a programmatic dependent that waits on the device for them.
+template <int D>
+int launch_combine(const fa::DecodeParams& p, int splits, void* o, float* lse, cudaStream_t stream) {
   fa::CombineParams cp{};
   cp.o_part = p.o_part;
   cp.lse_part = p.lse_part;
@@ -343,22 +367,21 @@ int launch_split_and_combine(const fa::DecodeParams& p, int keys, int outer, voi
   cp.lse = lse;
   cp.B = p.B;
   cp.Hq = p.Hq;
-  cp.splits = p.splits;
-  // The merge is a programmatic dependent launch: its CTAs may be scheduled while the split
-  // kernel drains, and wait on the device (griddepcontrol.wait) for the partials.
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(p.B) * p.Hq + 3) / 4));
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fa::fa_decode_combine_kernel<D>, cp) != cudaSuccess)
-    return FA_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  cp.splits = splits;
+  const unsigned blocks = static_cast<unsigned>((static_cast<long long>(p.B) * p.Hq + 3) / 4);
+  return launch(fa::fa_decode_combine_kernel<D>, dim3(blocks), 128, 0, true, stream, cp);
+}
+
+// The split kernel, then the merge kernel.  `keys` is the extent of the key axis of the code tensors
+// (Skv, or the page size), `outer` that of the last axis (B, or the number of pages).
+template <int D, bool kPaged, int kBits>
+int launch_split_and_combine(const fa::DecodeParams& p, int keys, int outer, void* o, float* lse,
+                             cudaStream_t stream) {
+  CodeMaps maps;
+  int rc = encode_codes(&maps, p.k, p.v, D * kBits / 8, p.Hkv, keys, outer, kPaged);
+  if (rc != FA_OK) return rc;
+  if ((rc = launch_split<D, kPaged, kBits>(maps, p, false, stream)) != FA_OK) return rc;
+  return launch_combine<D>(p, p.splits, o, lse, stream);
 }
 
 template <int D, int kBits>
@@ -496,13 +519,23 @@ int decode_paged(int bits, const void* q, const void* k, const void* v, const fl
 
 constexpr int kSms = 148;
 
-// Splits of the prefix: one CTA per SM runs a split of one (KV head, row block) in about
-// (tiles + 3) tile times (start-up, epilogue and its share of the merge count for three), in
-// as many waves as the CTAs need; the split count with the least total time, the smaller of equals.
+// Up to this many query rows per KV head, the prefix goes through the split kernel as well (8 rows a
+// CTA, its blocks of rows re-reading the tile from L2); above, the tcgen05 kernel's tile of
+// 128 rows pays.
+constexpr int kSharedFewRows = 16;
+
+// Splits of the prefix.  Few rows: three CTAs of the split kernel per SM.  Otherwise one CTA per SM
+// runs a split of one (KV head, row block) in about (tiles + 3) tile times (start-up, epilogue and
+// its share of the merge count for three), in as many waves as the CTAs need; the split count with
+// the least total time, the smaller of equals.
 int shared_prefix_splits(int B, int Hq, int Hkv, long long max_keys) {
   const long long R = static_cast<long long>(B) * (Hq / Hkv);
-  const long long base = static_cast<long long>(Hkv) * (R <= 128 ? 1 : (R + 255) / 256);
   const long long tiles = std::max(1ll, (max_keys + 127) / 128);
+  if (R <= kSharedFewRows) {
+    const long long ctas = Hkv * ((R + 7) / 8);
+    return static_cast<int>(std::min(tiles, std::max(1ll, 3 * kSms / ctas)));
+  }
+  const long long base = static_cast<long long>(Hkv) * (R <= 128 ? 1 : (R + 255) / 256);
   int best = 1;
   long long best_cost = -1;
   for (int s = 1; s <= kSms && s <= tiles; ++s) {
@@ -526,20 +559,14 @@ std::atomic<uint64_t> g_attr_shared[8];
 std::atomic<int> g_shared_regs[8] = {};  // registers per thread of each variant, 0 = not read
 
 template <int D, int kBits, bool kStream>
-int launch_shared_prefix(const fa::SharedParams& p, const void* k, const void* v,
-                         cudaStream_t stream) {
+int launch_shared_prefix(const CodeMaps& maps, const fa::SharedParams& p, cudaStream_t stream) {
   using C = fa::SharedCfg<D, kBits, kStream>;
   const long long grid = static_cast<long long>(p.Hkv) * p.row_blocks * p.splits;
   if (grid > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
-  CUtensorMap tk, tv;
-  const int page = 1 << p.page_shift;
-  const uint32_t box = static_cast<uint32_t>(std::min(128, page));
-  int rc;
-  if ((rc = encode_u8_4d(&tk, k, C::kRow, p.Hkv, page, p.num_pages, box)) != FA_OK) return rc;
-  if ((rc = encode_u8_4d(&tv, v, C::kRow, p.Hkv, page, p.num_pages, box)) != FA_OK) return rc;
   auto kernel = fa::fa_shared_prefix_kernel<D, kBits, kStream>;
   constexpr int variant = (D == 128 ? 4 : 0) + (kBits == 4 ? 2 : 0) + (kStream ? 1 : 0);
-  if ((rc = ensure_smem_attr(kernel, C::kSmemBytes, g_attr_shared[variant])) != FA_OK) return rc;
+  const int rc = ensure_smem_attr(kernel, C::kSmemBytes, g_attr_shared[variant]);
+  if (rc != FA_OK) return rc;
   // setmaxnreg redistributes the launch's registers; it only completes if they cover the split
   int regs = g_shared_regs[variant].load(std::memory_order_acquire);
   if (regs == 0) {
@@ -549,30 +576,38 @@ int launch_shared_prefix(const fa::SharedParams& p, const void* k, const void* v
     g_shared_regs[variant].store(regs, std::memory_order_release);
   }
   if (regs < C::kLaunchRegs) return FA_ERR_UNSUPPORTED;
-  kernel<<<static_cast<unsigned>(grid), C::kThreads, C::kSmemBytes, stream>>>(tk, tv, p);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch(kernel, dim3(static_cast<unsigned>(grid)), C::kThreads, C::kSmemBytes, true, stream,
+                maps.k, maps.v, p);
 }
 
+// The own keys' partials, beside them (a programmatic dependent that reads nothing of it, and does not
+// end before it) the prefix's, then the merge of both.
 template <int D, int kBits>
-int launch_shared(fa::DecodeParams own, fa::SharedParams sp, void* o, float* lse,
+int launch_shared(const fa::DecodeParams& own, const fa::SharedParams& sp, void* o, float* lse,
                   cudaStream_t stream) {
-  // the own keys' partials come first, those of the prefix behind them
-  int rc = launch_split<D, true, kBits>(own, 1 << own.page_shift, own.num_pages, stream);
+  CodeMaps maps;
+  int rc = encode_codes(&maps, own.k, own.v, D * kBits / 8, own.Hkv, 1 << own.page_shift,
+                        own.num_pages, true);
   if (rc != FA_OK) return rc;
-  rc = sp.R <= 128 ? launch_shared_prefix<D, kBits, true>(sp, own.k, own.v, stream)
-                   : launch_shared_prefix<D, kBits, false>(sp, own.k, own.v, stream);
+  if ((rc = launch_split<D, true, kBits>(maps, own, false, stream)) != FA_OK) return rc;
+  if (sp.R <= kSharedFewRows) {
+    fa::DecodeParams pre = own;  // one sequence of R rows
+    pre.B = 1;
+    pre.G = sp.R;
+    pre.splits = sp.splits;
+    pre.block_table = sp.table;
+    pre.seqlens = sp.len;
+    pre.max_pages = sp.max_pages;
+    pre.o_part = sp.o_part;
+    pre.lse_part = sp.lse_part;
+    rc = launch_split<D, true, kBits>(maps, pre, true, stream);
+  } else if (sp.R <= 128) {
+    rc = launch_shared_prefix<D, kBits, true>(maps, sp, stream);
+  } else {
+    rc = launch_shared_prefix<D, kBits, false>(maps, sp, stream);
+  }
   if (rc != FA_OK) return rc;
-  fa::CombineParams cp{};
-  cp.o_part = own.o_part;
-  cp.lse_part = own.lse_part;
-  cp.o = static_cast<uint16_t*>(o);
-  cp.lse = lse;
-  cp.B = own.B;
-  cp.Hq = own.Hq;
-  cp.splits = own.splits + sp.splits;
-  const long long rows = static_cast<long long>(own.B) * own.Hq;
-  fa::fa_shared_combine_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(cp);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_combine<D>(own, own.splits + sp.splits, o, lse, stream);
 }
 
 int page_shift_of(int page_size) {

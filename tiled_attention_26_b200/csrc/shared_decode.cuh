@@ -7,7 +7,7 @@
 //   x_rj = scale * k_scale_j * (q_r . kcode_j),   O_r = sum_j p_rj * v_scale_j * vcode_j
 // (the codes take part without being decompressed first: "Flash Attention on Ascend: three
 // techniques", section 3).  The keys each sequence owns go through the paged split kernel of
-// decode.cuh; both write partial outputs with their log-sum-exp, and fa_shared_combine_kernel
+// decode.cuh; both write partial outputs with their log-sum-exp, and fa_decode_combine_kernel
 // merges them: L = log sum_s exp(L_s), O = sum_s exp(L_s - L) O_s.
 //
 // fa_shared_prefix_kernel, one CTA per (KV head, block of rows, split of the prefix), 512 threads:
@@ -15,8 +15,9 @@
 //   warps 8-11  dequantisation: thread = key; K codes to fp16 (exact), V codes times their scale to
 //               fp16, both into the swizzled layout the tensor core reads
 //   warp 12     TMA producer: K and V code tiles of 128 keys, one box per page piece
+//   warp 14     the keys' scales, and the exponent E below
 //   warp 13     allocates TMEM and issues tcgen05.mma from one thread: S_t = Q_t K^T,
-//               O_t += P_t V with P_t from TMEM;  warps 14-15 idle
+//               O_t += P_t V with P_t from TMEM;  warp 15 idles
 // The two S tiles are two blocks of 128 query rows that share every K/V tile (kStream = false), or,
 // when R <= 128, two interleaved streams of key tiles over one block of rows (kStream = true), merged
 // in shared memory at the end; either way one tile's softmax runs while the tensor core works on
@@ -65,9 +66,9 @@ struct SharedCfg {
   static constexpr int kVOff = kKOff + 2 * kTile;
   static constexpr int kRawKOff = kVOff + 2 * kTile;
   static constexpr int kRawVOff = kRawKOff + kRaw * kRawTile;
-  static constexpr int kScaleOff = kRawVOff + kRaw * kRawTile;  // fp32 k_scale [4 tiles][128]
-  static constexpr int kVmaxOff = kScaleOff + 4 * 128 * 4;      // fp32 largest v_scale [4][4 warps]
-  static constexpr int kLseOff = kVmaxOff + 4 * 4 * 4;          // fp32 [128], kStream only
+  static constexpr int kScaleOff = kRawVOff + kRaw * kRawTile;  // fp32 [2 tiles][k, v][128]
+  static constexpr int kExpOff = kScaleOff + 2 * 2 * 512;       // int [2 tiles] V's exponent
+  static constexpr int kLseOff = kExpOff + 16;                  // fp32 [128], kStream only
   static constexpr int kBarOff = kLseOff + (kStream ? 512 : 0);
   static constexpr int kBarQ = 0;                    // [2]
   static constexpr int kBarRawKFull = 2;             // [kRaw]
@@ -78,8 +79,8 @@ struct SharedCfg {
   static constexpr int kBarVFull = kBarKFull + 2;
   static constexpr int kBarKEmpty = kBarVFull + 2;
   static constexpr int kBarVEmpty = kBarKEmpty + 2;
-  static constexpr int kBarScale = kBarVEmpty + 2;   // [4]
-  static constexpr int kBarSFull = kBarScale + 4;    // [2]
+  static constexpr int kBarScale = kBarVEmpty + 2;   // [2]
+  static constexpr int kBarSFull = kBarScale + 2;    // [2]
   static constexpr int kBarPFull = kBarSFull + 2;    // [2 tiles][2 halves]
   static constexpr int kBarOFinal = kBarPFull + 4;   // [2]
   static constexpr int kBarDrain = kBarOFinal + 2;
@@ -167,6 +168,7 @@ __global__ void __launch_bounds__(512, 1)
     fa_shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v, const SharedParams p) {
   using C = SharedCfg<D, kBits, kStream>;
+  asm volatile("griddepcontrol.launch_dependents;");  // (the merge waits on the device)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // the swizzled tiles need 1024-byte aligned shared memory, and there is no room to align it here
   if ((smem_u32(smem_raw) & 1023u) != 0) {
@@ -212,6 +214,7 @@ __global__ void __launch_bounds__(512, 1)
   if (nt == 0) {
     for (int r = threadIdx.x; r < live; r += blockDim.x)
       p.lse_part[split * rows + out_row(r)] = -INFINITY;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // (as below)
     return;
   }
   const bool act1 = kStream ? nt > 1 : live > 128;  // S tile 1 has work
@@ -220,9 +223,7 @@ __global__ void __launch_bounds__(512, 1)
     for (int i = 0; i < C::kNumBars; ++i) {
       uint32_t count = 1;
       if (i < 2 || (i >= C::kBarPFull && i < C::kBarPFull + 4)) count = 128;
-      if ((i >= C::kBarRawKEmpty && i < C::kBarKEmpty) ||
-          (i >= C::kBarScale && i < C::kBarScale + 4))
-        count = 4;
+      if (i >= C::kBarRawKEmpty && i < C::kBarKEmpty) count = 4;
       mbar_init(bar(i), count);
     }
     *abort_flag = 0;
@@ -241,8 +242,7 @@ __global__ void __launch_bounds__(512, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  auto checked_page = [&](int slot) -> int {
-    int pg = p.table[slot];
+  auto checked_page = [&](int pg) -> int {
     if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.num_pages)) {
       atomicOr(&g_fa_device_status, kDevStatusBadIndex);
       pg = 0;
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(512, 1)
       const uint64_t pol = l2_evict_first_policy();
       auto page_at = [&](int j) -> int {
         const int t = t_begin + 128 * j + lane * box_t;
-        return lane < boxes && j < nt && t < t_end ? checked_page(t >> p.page_shift) : -1;
+        return lane < boxes && j < nt && t < t_end ? checked_page(p.table[t >> p.page_shift]) : -1;
       };
       int pg = page_at(0), issued = 0;
       bool ok = true;
@@ -306,6 +306,63 @@ __global__ void __launch_bounds__(512, 1)
             mbar_wait(bar((kind ? C::kBarRawVFull : C::kBarRawKFull) + s),
                       ((n - 1 - s) / C::kRaw) & 1, drain_ctl);
         }
+      }
+    } else if (warp == 14) {
+      // ================= scales: lane i has keys 4 i .. 4 i + 3 of each tile =================
+      // k_scale as it is, v_scale times 2^E; keys past the prefix count 0.  Table entries are read two
+      // tiles ahead, scales one ahead.
+      const int pmask = (1 << p.page_shift) - 1;
+      auto entry_at = [&](int j) -> int {
+        const int t = t_begin + 128 * j + 4 * lane;
+        return j < nt && t < t_end ? __ldg(p.table + (t >> p.page_shift)) : 0;
+      };
+      auto scales_at = [&](int j, int entry, float4& ks, float4& vs) {
+        const int t = t_begin + 128 * j + 4 * lane;
+        ks = vs = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < nt && t < t_end) {
+          const size_t at =
+              ((static_cast<size_t>(checked_page(entry)) * p.Hkv + kvh) << p.page_shift) + (t & pmask);
+          ks = __ldg(reinterpret_cast<const float4*>(p.k_scale + at));
+          vs = __ldg(reinterpret_cast<const float4*>(p.v_scale + at));
+        }
+      };
+      float4 ks, vs, ks_next, vs_next;
+      scales_at(0, entry_at(0), ks, vs);
+      int entry = entry_at(1);
+      constexpr int kUnset = 1 << 20;
+      int e0 = kUnset, e1 = kUnset;  // exponents of the accumulators of this tile and of the next
+      for (int j = 0; j < nt; ++j) {
+        scales_at(j + 1, entry, ks_next, vs_next);
+        entry = entry_at(j + 2);
+        const int left = t_end - (t_begin + 128 * j + 4 * lane);
+        if (left < 4) {  // the page's scales behind the prefix may be anything
+          if (left < 1) ks.x = vs.x = 0.f;
+          if (left < 2) ks.y = vs.y = 0.f;
+          if (left < 3) ks.z = vs.z = 0.f;
+          ks.w = vs.w = 0.f;
+        }
+        const uint32_t kAbs = 0x7fffffffu;
+        const uint32_t top = __reduce_max_sync(
+            0xffffffffu, max(max(__float_as_uint(vs.x) & kAbs, __float_as_uint(vs.y) & kAbs),
+                             max(__float_as_uint(vs.z) & kAbs, __float_as_uint(vs.w) & kAbs)));
+        const int e = min(e0, exponent_below(__uint_as_float(top), 8));
+        e0 = kStream ? e1 : e;
+        e1 = e;
+        const float f = exp2i(e);
+        const int slot = j & 1;
+        const uint32_t dst = sb + C::kScaleOff + slot * 1024 + 16 * lane;
+        // the slot is free once the products of tile j - 2 are done
+        const bool ok = mbar_wait(bar(C::kBarVEmpty + slot), ((j >> 1) & 1) ^ 1, ctl);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        sts128(dst, __float_as_uint(ks.x), __float_as_uint(ks.y), __float_as_uint(ks.z),
+               __float_as_uint(ks.w));
+        sts128(dst + 512, __float_as_uint(vs.x * f), __float_as_uint(vs.y * f),
+               __float_as_uint(vs.z * f), __float_as_uint(vs.w * f));
+        if (lane == 0) reinterpret_cast<volatile int*>(smem + C::kExpOff)[slot] = e;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kBarScale + slot));
+        ks = ks_next;
+        vs = vs_next;
       }
     } else if (warp == 13 && lane == 0) {
       // ================= MMA issuer =================
@@ -405,38 +462,11 @@ __global__ void __launch_bounds__(512, 1)
   } else if (warp >= 8) {
     setmaxnreg_dec<C::kRegsDequant>();
     // ================= dequantisation: thread r = key r of each tile =================
-    const int r = threadIdx.x & 127, w4 = warp & 3;
-    const int pmask = (1 << p.page_shift) - 1;
-    // page of this thread's key of tile j (-1: past the prefix), two tiles ahead; scales one ahead
-    auto page_at = [&](int j) -> int {
-      const int t = t_begin + 128 * j + r;
-      return j < nt && t < t_end ? checked_page(t >> p.page_shift) : -1;
-    };
-    auto scale_at = [&](const float* s, int j, int pg) -> float {
-      if (pg < 0) return 0.f;
-      const int t = t_begin + 128 * j + r;
-      return __ldg(s + (((static_cast<size_t>(pg) * p.Hkv + kvh) << p.page_shift) + (t & pmask)));
-    };
-    int pg = page_at(0);
-    float ks = scale_at(p.k_scale, 0, pg), vs = scale_at(p.v_scale, 0, pg);
-    pg = page_at(1);
-    constexpr int kUnset = 1 << 20;
-    int E[2] = {kUnset, kUnset};  // of the accumulators the tile goes to
+    const int r = threadIdx.x & 127;
     for (int j = 0; j < nt; ++j) {
-      const float ks_next = scale_at(p.k_scale, j + 1, pg), vs_next = scale_at(p.v_scale, j + 1, pg);
-      pg = page_at(j + 2);
-      const int s = j % C::kRaw, ph = (j / C::kRaw) & 1, slot = j & 1;
-      // --- K: the slot's last reader is done, so is everyone with this entry of the scale ring ---
-      bool ok = mbar_wait(bar(C::kBarKEmpty + slot), ((j >> 1) & 1) ^ 1, ctl);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      float* ring = reinterpret_cast<float*>(smem + C::kScaleOff) + (j & 3) * 128;
-      float* vmax = reinterpret_cast<float*>(smem + C::kVmaxOff) + (j & 3) * 4;
-      ring[r] = ks;
-      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(vs)));
-      if (lane == 0) vmax[w4] = __uint_as_float(top);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::kBarScale + (j & 3)));
-      ok = mbar_wait(bar(C::kBarRawKFull + s), ph, ctl);
+      const int s = j % C::kRaw, ph = (j / C::kRaw) & 1, slot = j & 1, use = (j >> 1) & 1;
+      bool ok = mbar_wait(bar(C::kBarKEmpty + slot), use ^ 1, ctl) &&
+                mbar_wait(bar(C::kBarRawKFull + s), ph, ctl);
       if (!__all_sync(0xffffffffu, ok)) break;
       dequant_row<D, kBits, false>(sb + C::kRawKOff + s * C::kRawTile,
                                    sb + C::kKOff + slot * C::kTile, r, 0u, 0u);
@@ -446,27 +476,21 @@ __global__ void __launch_bounds__(512, 1)
         mbar_arrive(bar(C::kBarRawKEmpty + s));
         mbar_arrive(bar(C::kBarKFull + slot));
       }
-      // --- V: times v_scale * 2^E ---
-      ok = mbar_wait(bar(C::kBarScale + (j & 3)), (j >> 2) & 1, ctl) &&
-           mbar_wait(bar(C::kBarRawVFull + s), ph, ctl) &&
-           mbar_wait(bar(C::kBarVEmpty + slot), ((j >> 1) & 1) ^ 1, ctl);
+      // (the scales' slot is written after V's is free)
+      ok = mbar_wait(bar(C::kBarScale + slot), use, ctl) &&
+           mbar_wait(bar(C::kBarRawVFull + s), ph, ctl);
       if (!__all_sync(0xffffffffu, ok)) break;
-      const float4 vm = *reinterpret_cast<const float4*>(vmax);
-      int& e = E[kStream ? slot : 0];
-      e = min(e, exponent_below(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)), 8));
-      const float vsx = vs * exp2i(e);
+      const float vs = lds32f(sb + C::kScaleOff + slot * 1024 + 512 + 4 * r);
       dequant_row<D, kBits, true>(sb + C::kRawVOff + s * C::kRawTile,
-                                  sb + C::kVOff + slot * C::kTile, r, pack_f16x2(vsx, vsx),
-                                  kBits == 4 ? pack_f16x2(vsx * 0.0625f, vsx * 0.0625f)
-                                             : pack_f16x2(vsx, vsx));
+                                  sb + C::kVOff + slot * C::kTile, r, pack_f16x2(vs, vs),
+                                  kBits == 4 ? pack_f16x2(vs * 0.0625f, vs * 0.0625f)
+                                             : pack_f16x2(vs, vs));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(C::kBarRawVEmpty + s));
         mbar_arrive(bar(C::kBarVFull + slot));
       }
-      ks = ks_next;
-      vs = vs_next;
     }
   } else {
     setmaxnreg_inc<C::kRegsSoftmax>();
@@ -482,15 +506,13 @@ __global__ void __launch_bounds__(512, 1)
 
     float sc = 0.f;  // score units: log2, undoing the row's power of two
     {
-      uint4 x[D / 8];
       const uint4* src = reinterpret_cast<const uint4*>(p.q + out_row(min(R, live - 1)) * D);
       uint32_t am = 0;
-#pragma unroll
+#pragma unroll 4
       for (int c = 0; c < D / 8; ++c) {
-        x[c] = R < live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        const uint4 x = R < live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
         const uint32_t kAbs = 0x7fff7fffu;
-        am = __vmaxu2(am, __vmaxu2(__vmaxu2(x[c].x & kAbs, x[c].y & kAbs),
-                                   __vmaxu2(x[c].z & kAbs, x[c].w & kAbs)));
+        am = __vmaxu2(am, __vmaxu2(__vmaxu2(x.x & kAbs, x.y & kAbs), __vmaxu2(x.z & kAbs, x.w & kAbs)));
       }
       const int eq = exponent_below(__uint_as_float(max(am & 0xffffu, am >> 16) << 16), 15);
       const float qs = exp2i(eq);
@@ -500,9 +522,10 @@ __global__ void __launch_bounds__(512, 1)
         const uint32_t row = sb + C::kQOff + (kStream ? 0 : t) * C::kTile + r * 128;
         // INT4: the K operand's dim order, and 1/16 for its 16 x codes
         const float qh = kBits == 4 ? qs * 0.0625f : qs;
-#pragma unroll
+#pragma unroll 2  // (short code: it runs once, from a cold instruction cache)
         for (int c = 0; c < D / 8; ++c) {
-          const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+          const uint4 x = R < live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
           float f[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -541,11 +564,13 @@ __global__ void __launch_bounds__(512, 1)
       uint32_t sv[4][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(trow + colS + 32 * c, sv[c]);
-      ok = mbar_wait(bar(C::kBarScale + (j & 3)), (j >> 2) & 1, ctl);
+      ok = mbar_wait(bar(C::kBarScale + (j & 1)), (j >> 1) & 1, ctl);
       if (!__all_sync(0xffffffffu, ok)) break;
+      const int e_new = static_cast<int>(lds32(sb + C::kExpOff + 4 * (j & 1)));
       tmem_wait_ld();
-      // raw scores times k_scale (the row's common factor sc joins in the exponent)
-      const uint32_t ring = sb + C::kScaleOff + (j & 3) * 512;
+      // raw scores times k_scale (the row's common factor sc joins in the exponent), and their maximum
+      const uint32_t ring = sb + C::kScaleOff + (j & 1) * 1024;
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -562,31 +587,22 @@ __global__ void __launch_bounds__(512, 1)
           sv[c][4 * q4 + 1] = __float_as_uint(a1);
           sv[c][4 * q4 + 2] = __float_as_uint(b0);
           sv[c][4 * q4 + 3] = __float_as_uint(b1);
+          mx[2 * (q4 & 1)] = fmax3(mx[2 * (q4 & 1)], a0, a1);
+          mx[2 * (q4 & 1) + 1] = fmax3(mx[2 * (q4 & 1) + 1], b0, b1);
         }
+      float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       const int limit = t_end - (t_begin + 128 * j);
       if (limit < 128) {
+        top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
+          for (int k = 0; k < 32; ++k) {
             if (32 * c + k >= limit) sv[c][k] = __float_as_uint(-INFINITY);
+            top = fmaxf(top, __uint_as_float(sv[c][k]));
+          }
       }
-      float mx[8];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) mx[c] = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int col = 16 * i + 2 * c;
-          mx[c] = fmax3(mx[c], __uint_as_float(sv[col / 32][col % 32]),
-                        __uint_as_float(sv[(col + 1) / 32][(col + 1) % 32]));
-        }
-      const float m_new = fmaxf(m, fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
-                                         fmaxf(mx[6], mx[7])) * sc);
-      const float4 vm = *reinterpret_cast<const float4*>(smem + C::kVmaxOff + (j & 3) * 16);
-      const int e_new =
-          min(E, exponent_below(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)), 8));
+      const float m_new = fmaxf(m, top * sc);
       // O is rescaled when the maximum grew by more than 2^8 (until then the old one stays the
       // reference and p may reach 2^8) or V's exponent fell
       float alpha = 1.f;
@@ -603,14 +619,14 @@ __global__ void __launch_bounds__(512, 1)
       }
       if (__any_sync(0xffffffffu, resc)) {
         const float a = alpha * exp2i_or_zero(e_new - E);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t ov[32];
-          tmem_ld32(trow + colO + 32 * c, ov);
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t ov[16];
+          tmem_ld16(trow + colO + 16 * c, ov);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * a);
-          tmem_st32(trow + colO + 32 * c, ov);
+          for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * a);
+          tmem_st16(trow + colO + 16 * c, ov);
         }
       }
       E = e_new;
@@ -658,13 +674,15 @@ __global__ void __launch_bounds__(512, 1)
     float lse2 = some ? m + (log2f(l) - 7.f) : -INFINITY;
     float w0 = 1.f, w1 = 0.f;
     float* lse_x = reinterpret_cast<float*>(smem + C::kLseOff);
-    // stream 1 leaves its normalised rows in the K and V slots that only it used (every product
-    // of its tiles has completed), D / 2 dims in each, 16-byte pieces XORed with the row
-    auto x_addr = [&](int d) {  // of dims d .. d + 3
+    // Rows are staged in shared memory, to be written to global memory row by row, and so that stream 0
+    // can add stream 1's.  What is free by now: tile 0's products of QK^T and its own of PV are done
+    // (K's slots), tile 1's last of all (V's slots); streams each have a slot of K and of V to
+    // themselves.  Half of a row's dims in each of the two areas, 16-byte pieces XORed with the row.
+    const uint32_t area0 = sb + (kStream ? C::kKOff + t * C::kTile : t ? C::kVOff : C::kKOff);
+    const uint32_t area1 = kStream ? sb + C::kVOff + t * C::kTile : area0 + C::kTile;
+    auto piece = [&](uint32_t a0, uint32_t a1, int row, int d) {  // of dims d .. d + 3
       constexpr int kHalf = D / 2;
-      const int q = (d % kHalf) / 4;
-      return sb + (d < kHalf ? C::kKOff : C::kVOff) + C::kTile + r * (kHalf * 4) +
-             ((q ^ (r & 7)) << 4);
+      return (d < kHalf ? a0 : a1) + row * (kHalf * 4) + ((((d % kHalf) / 4) ^ (row & 7)) << 4);
     };
     if constexpr (kStream) {
       if (t == 1) lse_x[r] = lse2;
@@ -681,10 +699,8 @@ __global__ void __launch_bounds__(512, 1)
         w1 *= inv;
       }
     }
-    const size_t orow = out_row(min(R, live - 1));
-    float* dst = p.o_part + (split * rows + orow) * D;
     if (warp_live) {
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t ov[32];
         if (have) {
@@ -701,31 +717,41 @@ __global__ void __launch_bounds__(512, 1)
             f[dim] = some ? __uint_as_float(ov[8 * q8 + i]) * inv_l * unscale : 0.f;
           }
           const int d = 32 * c + 8 * q8;
-          if (kStream && t == 1) {
-            sts128(x_addr(d), __float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                   __float_as_uint(f[3]));
-            sts128(x_addr(d + 4), __float_as_uint(f[4]), __float_as_uint(f[5]),
-                   __float_as_uint(f[6]), __float_as_uint(f[7]));
-          } else {
-            if constexpr (kStream) {
-              if (act1) {
-                const uint4 y0 = lds128(x_addr(d)), y1 = lds128(x_addr(d + 4));
-                const uint32_t y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+          if constexpr (kStream) {
+            if (t == 0 && act1) {
+              const uint32_t b0 = area0 + C::kTile, b1 = area1 + C::kTile;  // stream 1's
+              const uint4 y0 = lds128(piece(b0, b1, r, d)), y1 = lds128(piece(b0, b1, r, d + 4));
+              const uint32_t y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = w0 * f[i] + w1 * __uint_as_float(y[i]);
-              }
-            }
-            if (R < live) {
-              *reinterpret_cast<float4*>(dst + d) = make_float4(f[0], f[1], f[2], f[3]);
-              *reinterpret_cast<float4*>(dst + d + 4) = make_float4(f[4], f[5], f[6], f[7]);
+              for (int i = 0; i < 8; ++i) f[i] = w0 * f[i] + w1 * __uint_as_float(y[i]);
             }
           }
+          sts128(piece(area0, area1, r, d), __float_as_uint(f[0]), __float_as_uint(f[1]),
+                 __float_as_uint(f[2]), __float_as_uint(f[3]));
+          sts128(piece(area0, area1, r, d + 4), __float_as_uint(f[4]), __float_as_uint(f[5]),
+                 __float_as_uint(f[6]), __float_as_uint(f[7]));
         }
       }
     }
     if (kStream && t == 1) named_bar_sync(1, 256);
-    if ((!kStream || t == 0) && R < live)
-      p.lse_part[split * rows + orow] = lse2 * 0.69314718055994531f;
+    if ((!kStream || t == 0) && warp_live) {
+      __syncwarp();
+      const int orow = static_cast<int>(out_row(min(R, live - 1)));
+      // Launched as a programmatic dependent of the kernel that reads the sequences' own keys: this grid
+      // does not end before that one, so whoever waits for this one waits for both.
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (R < live) p.lse_part[split * rows + orow] = lse2 * 0.69314718055994531f;
+      constexpr int kLanes = D / 4;  // lanes of a row
+      const int mine = 4 * (lane % kLanes);
+#pragma unroll 4
+      for (int i = 0; i < 32; i += 32 / kLanes) {
+        const int w = i + lane / kLanes;
+        const int to = __shfl_sync(0xffffffffu, orow, w);
+        const uint4 x = lds128(piece(area0, area1, (r & ~31) + w, mine));
+        if ((R & ~31) + w < live)
+          *reinterpret_cast<uint4*>(p.o_part + (split * rows + to) * D + mine) = x;
+      }
+    }
   }
 
   tc_fence_before();
@@ -735,41 +761,6 @@ __global__ void __launch_bounds__(512, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
-}
-
-// One warp per (sequence, query head): merges `splits` partials (those of the sequence's own keys,
-// then those of the prefix).  A partial with log-sum-exp -inf holds no key and is not read.
-template <int D>
-__global__ void __launch_bounds__(128) fa_shared_combine_kernel(const CombineParams p) {
-  constexpr int V = D / 32;  // dims per lane
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int rows = p.B * p.Hq;
-  if (row >= rows) return;
-  float top = -INFINITY;
-  for (int s = lane; s < p.splits; s += 32)
-    top = fmaxf(top, p.lse_part[static_cast<size_t>(s) * rows + row]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float sum = 0.f, acc[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
-    const size_t at = static_cast<size_t>(s) * rows + row;
-    const float ls = p.lse_part[at];
-    if (ls == -INFINITY) continue;
-    const float w = expf(ls - top);
-    sum += w;
-    const float* src = p.o_part + at * D + V * lane;
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] += w * src[i];
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint16_t* dst = p.o + static_cast<size_t>(row) * D + V * lane;
-#pragma unroll
-  for (int i = 0; i < V; i += 2)
-    *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
 }
 
 }  // namespace fa
