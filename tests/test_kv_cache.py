@@ -209,6 +209,32 @@ def test_contiguous_matches_definition(built, bits, B, S, Hkv, D, kind):
         assert same_values(_bits(val), values_bits(c, s))
 
 
+@gpu
+@pytest.mark.parametrize("bits", [8, 4])
+def test_every_quotient_of_mantissas(built, bits):
+    """Rows whose largest value has each of the 128 mantissas, against every bf16 of a smaller or equal size
+    that can round to a code other than 0: quotients on and next to a half among them.  A power of two in
+    front changes nothing: small, large, and where 1 / scale would leave the normal range."""
+    m = 127 if bits == 8 else 7
+    x = np.arange(0x3f80 - 10 * 128, 0x4000, dtype=np.uint16)  # 2^-10 .. 2
+    x = np.concatenate([x, x | 0x8000])
+    rows = []
+    for top in range(0x3f80, 0x4000):
+        fit = x[(x & 0x7fff) <= top]
+        fit = np.concatenate([fit, np.zeros(-len(fit) % 127, np.uint16)]).reshape(-1, 127)
+        rows.append(np.concatenate([fit, np.full((len(fit), 1), top, np.uint16)], 1))
+    rows = np.concatenate(rows)
+    rows = np.concatenate([rows, np.zeros((-len(rows) % 3, 128), np.uint16)])
+    for e in (0, 126, -30, -100, -116):
+        b = rows if e == 0 else (bf16_to_f64(rows) * 2.0 ** e).astype(np.float32).view(np.uint32) >> 16
+        b = b.astype(np.uint16).reshape(1, -1, 3, 128)
+        codes, scale = quantize_f64(b, m)
+        got = _call("quantize", bits)(_bf16(b), _bf16(b[:, ::-1].copy()))
+        assert np.array_equal(got[0].cpu().numpy(), pack(codes, bits))
+        assert np.array_equal(got[1].cpu().numpy(), pack(codes, bits)[:, ::-1])
+        assert np.array_equal(got[2].cpu().numpy(), scale.transpose(0, 2, 1))
+
+
 PAGED = [  # bits, Hkv, D, P, history, new tokens, padding rows
     (8, 8, 128, 64, [0], [1], 0),
     (8, 2, 128, 16, [0, 15, 16, 31], [1, 1, 1, 1], 0),

@@ -107,9 +107,15 @@ def fa_status_string(status: int) -> str:
 def _stream_ptr(stream):
     import torch
     if stream is None:
-        # (the pointer alone: building a Stream object costs several microseconds a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _current_stream_ptr(torch.cuda.current_device())
     return stream.cuda_stream
+
+
+def _current_stream_ptr(index):
+    """The current stream of device ``index``, as its pointer alone (a Stream object costs
+    microseconds)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _check(t, name, dtype, shape, device):
@@ -355,6 +361,14 @@ def _on(dev, stream):
     return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
+def _buffer(t, name, dtype, shape, like):
+    """The caller's output ``t``, checked, or a new one on the device of ``like``."""
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    _check(t, name, dtype, shape, like.device)
+    return t
+
+
 def _code_type(bits, D):
     """dtype and elements of one row of D codes."""
     import torch
@@ -372,20 +386,15 @@ def _kv_quantize(bits, k, v, k_codes, v_codes, k_scale, v_scale, stream):
     _check(k, "k", torch.bfloat16, (B, S, Hkv, D), dev)
     _check(v, "v", torch.bfloat16, (B, S, Hkv, D), dev)
     with _on(dev, stream):
-        out = []
-        for t, what in ((k_codes, "k_codes"), (v_codes, "v_codes")):
-            t = torch.empty((B, S, Hkv, row), dtype=code, device=dev) if t is None else t
-            _check(t, what, code, (B, S, Hkv, row), dev)
-            out.append(t)
-        for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            t = torch.empty((B, Hkv, S), dtype=torch.float32, device=dev) if t is None else t
-            _check(t, what, torch.float32, (B, Hkv, S), dev)
-            out.append(t)
+        out = (_buffer(k_codes, "k_codes", code, (B, S, Hkv, row), k),
+               _buffer(v_codes, "v_codes", code, (B, S, Hkv, row), k),
+               _buffer(k_scale, "k_scale", torch.float32, (B, Hkv, S), k),
+               _buffer(v_scale, "v_scale", torch.float32, (B, Hkv, S), k))
         rc = getattr(lib(), name)(k.data_ptr(), v.data_ptr(), *(t.data_ptr() for t in out), B, S,
-                                  Hkv, D, _stream_ptr(None))
+                                  Hkv, D, _current_stream_ptr(dev.index))
     if rc != 0:
         raise FaError(rc, name)
-    return tuple(out)
+    return out
 
 
 def fa_kv_quantize_int8(k, v, k_codes=None, v_codes=None, k_scale=None, v_scale=None, stream=None):
@@ -414,13 +423,11 @@ def _kv_dequantize(bits, k_codes, v_codes, k_scale, v_scale, k, v, stream):
     _check(k_scale, "k_scale", torch.float32, (B, Hkv, S), dev)
     _check(v_scale, "v_scale", torch.float32, (B, Hkv, S), dev)
     with _on(dev, stream):
-        k = torch.empty((B, S, Hkv, D), dtype=torch.bfloat16, device=dev) if k is None else k
-        v = torch.empty((B, S, Hkv, D), dtype=torch.bfloat16, device=dev) if v is None else v
-        _check(k, "k", torch.bfloat16, (B, S, Hkv, D), dev)
-        _check(v, "v", torch.bfloat16, (B, S, Hkv, D), dev)
+        k = _buffer(k, "k", torch.bfloat16, (B, S, Hkv, D), k_codes)
+        v = _buffer(v, "v", torch.bfloat16, (B, S, Hkv, D), k_codes)
         rc = getattr(lib(), name)(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
                                   v_scale.data_ptr(), k.data_ptr(), v.data_ptr(), B, S, Hkv, D,
-                                  _stream_ptr(None))
+                                  _current_stream_ptr(dev.index))
     if rc != 0:
         raise FaError(rc, name)
     return k, v
@@ -500,7 +507,7 @@ def _kv_append(bits, k, v, k_pages, v_pages, k_scale_pages, v_scale_pages, block
             k_scale_pages.data_ptr(), v_scale_pages.data_ptr(), block_table.data_ptr(),
             positions.data_ptr() if positions is not None else None,
             cu_tokens.data_ptr() if cu_tokens is not None else None, n, B, Hkv, P, max_pages,
-            num_pages, D, _stream_ptr(None))
+            num_pages, D, _current_stream_ptr(dev.index))
     if rc != 0:
         raise FaError(rc, name)
 
@@ -538,16 +545,14 @@ def _kv_gather(bits, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table
     if n < 0:
         raise ValueError(f"num_tokens must not be negative, got {n}")
     with _on(dev, stream):
-        k = torch.empty((n, Hkv, D), dtype=torch.bfloat16, device=dev) if k is None else k
-        v = torch.empty((n, Hkv, D), dtype=torch.bfloat16, device=dev) if v is None else v
-        _check(k, "k", torch.bfloat16, (n, Hkv, D), dev)
-        _check(v, "v", torch.bfloat16, (n, Hkv, D), dev)
+        k = _buffer(k, "k", torch.bfloat16, (n, Hkv, D), k_pages)
+        v = _buffer(v, "v", torch.bfloat16, (n, Hkv, D), k_pages)
         rc = getattr(lib(), name)(
             k_pages.data_ptr(), v_pages.data_ptr(), k_scale_pages.data_ptr(),
             v_scale_pages.data_ptr(), block_table.data_ptr(),
             positions.data_ptr() if positions is not None else None,
             cu_tokens.data_ptr() if cu_tokens is not None else None, k.data_ptr(), v.data_ptr(),
-            n, B, Hkv, P, max_pages, num_pages, D, _stream_ptr(None))
+            n, B, Hkv, P, max_pages, num_pages, D, _current_stream_ptr(dev.index))
     if rc != 0:
         raise FaError(rc, name)
     return k, v
@@ -597,23 +602,22 @@ def _decode_shared(bits, q, k_pages, v_pages, k_scale_pages, v_scale_pages, pref
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     with _on(dev, stream):
-        o = torch.empty_like(q) if o is None else o
-        _check(o, "o", torch.bfloat16, (B, 1, Hq, D), dev)
-        if lse is None and return_lse:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-        if lse is not None:
-            _check(lse, "lse", torch.float32, (B, Hq), dev)
+        o = _buffer(o, "o", torch.bfloat16, (B, 1, Hq, D), q)
+        if lse is not None or return_lse:
+            lse = _buffer(lse, "lse", torch.float32, (B, Hq), q)
         if workspace is None:
-            need = fa_decode_shared_workspace_bytes(B, Hq, Hkv, D, max_prefix * P, max_pages * P,
-                                                    num_splits)
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+            need = lib().fa_decode_shared_workspace_bytes(B, Hq, Hkv, D, max_prefix * P,
+                                                          max_pages * P, num_splits)
+            workspace = q.new_empty(max(need, 1), dtype=torch.uint8)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {dev}")
         rc = getattr(lib(), name)(
             q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale_pages.data_ptr(),
             v_scale_pages.data_ptr(), prefix_table.data_ptr(), prefix_len.data_ptr(),
             block_table.data_ptr(), seqlens.data_ptr(), o.data_ptr(),
             lse.data_ptr() if lse is not None else None, B, Hq, Hkv, P, max_prefix, max_pages,
             num_pages, D, scale, num_splits, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream_ptr(None))
+            workspace.numel() * workspace.element_size(), _current_stream_ptr(dev.index))
     if rc != 0:
         raise FaError(rc, name)
     return o, lse

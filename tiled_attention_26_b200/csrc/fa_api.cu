@@ -618,17 +618,26 @@ int page_shift_of(int page_size) {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// One warp per (32 tokens, K or V, KV head), 8 warps per block.
-template <int D, int kBits, bool kPaged, bool kWrite>
-int launch_kv_copy(const fa::KvCopyParams& p, cudaStream_t stream) {
-  const long long units = (static_cast<long long>(p.map.N) + 31) / 32 * 2 * p.map.Hkv;
+// One warp per (kTokens tokens, K or V, KV head), 8 warps per block.
+template <int D, int kBits, bool kPaged, bool kWrite, int kTokens>
+int launch_kv_copy_tokens(const fa::KvCopyParams& p, cudaStream_t stream) {
+  const long long units = (static_cast<long long>(p.map.N) + kTokens - 1) / kTokens * 2 * p.map.Hkv;
   const long long grid = (units + 7) / 8;
   if (grid > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
   if (kWrite)
-    fa::fa_kv_write_kernel<D, kBits, kPaged><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
+    fa::fa_kv_write_kernel<D, kBits, kPaged, kTokens><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
   else
-    fa::fa_kv_read_kernel<D, kBits, kPaged><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
+    fa::fa_kv_read_kernel<D, kBits, kPaged, kTokens><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// Warps of 32 tokens where that makes enough of them (16 per SM); smaller calls are latency: as many
+// warps as the rows make.
+template <int D, int kBits, bool kPaged, bool kWrite>
+int launch_kv_copy(const fa::KvCopyParams& p, cudaStream_t stream) {
+  if (static_cast<long long>(p.map.N) * p.map.Hkv >= 8ll * 32 * kSms)
+    return launch_kv_copy_tokens<D, kBits, kPaged, kWrite, 32>(p, stream);
+  return launch_kv_copy_tokens<D, kBits, kPaged, kWrite, 512 / D>(p, stream);
 }
 
 template <int kBits, bool kPaged, bool kWrite>

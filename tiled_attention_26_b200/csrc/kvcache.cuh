@@ -11,7 +11,8 @@
 // [page][Hkv][P].  A contiguous cache [B, S, Hkv, ...] is the case P = S, page = sequence.
 //
 // Layout of the work: one warp takes 32 consecutive tokens of one KV head, of K or of V, so that
-// the 32 scales (consecutive in memory) move as one coalesced access, lane = token.  A row is
+// the 32 scales (consecutive in memory) move as one coalesced access, lane = token (a small call: the
+// tokens that the warp holds at once, so that more warps share it).  A row is
 // spread over D / 16 lanes, each with two 8-value chunks D / 2 apart, so every access of a row is
 // contiguous over its lanes; consecutive warps of a block take consecutive heads, which
 // are adjacent in memory.
@@ -97,125 +98,146 @@ __device__ __forceinline__ void kv_check_cu(const KvMap& m) {
   if (bad) atomicOr(&g_fa_device_status, kDevStatusBadIndex);
 }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-
-// Codes of the 8 bf16 values in x, one per low byte (two's complement) of c.  `exact`: every
-// quotient by an IEEE division.  Otherwise x * inv, inv = 1 / scale rounded, which is off the
-// quotient by less than 127 * 2^-22 < 2^-14: where it is nearer than that to halfway between two
-// codes, the caller runs the exact form instead; d collects the largest distance from a code.
-__device__ __forceinline__ void kv_codes8(const uint4& x, float inv, uint32_t (&c)[8], float& d) {
+// The codes of the 8 bf16 values in x as 8 bytes (INT8) or nibbles (INT4): rint(fl32(x / scale)),
+// with inv = 1 / scale rounded and nscale = -scale.  fl32(x / scale) comes from inv by two steps of
+// q + (x - q scale) inv: after the first q is off by less than a unit in the last place, after the
+// second it is the rounded quotient (P. Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990).  Quotients that fall on or near a half are common - x = max / 2
+// is one - so every value takes both.
+// kTiny: x is multiplied by f first, as the scale was.  2^96 keeps the residuals of rows with scales
+// below 2^-90 in the normal range (and changes no quotient); codes are clamped, for a scale below the
+// normal range can be far enough off max|x| / m for the quotient to pass m.
+template <int kBits, bool kTiny>
+__device__ __forceinline__ uint2 kv_codes8(const uint4& x, float inv, float nscale, float f) {
   constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float f = __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
-    const float t = fmaf(f, inv, kRound);
-    c[i] = __float_as_uint(t);
-    d = fmaxf(d, fabsf(fmaf(f, inv, kRound - t)));
-  }
-}
-
-template <int kBits>
-__device__ __forceinline__ void kv_codes8_exact(const uint4& x, float scale, uint32_t (&c)[8]) {
   constexpr float m = kBits == 8 ? 127.f : 7.f;
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const uint64_t inv2 = f2(inv, inv), ns2 = f2(nscale, nscale), round2 = f2(kRound, kRound);
+  uint32_t c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float f = __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
-    // (a scale below the normal range can be far enough off max|x| / m to pass it)
-    c[i] = static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(f, scale)), -m), m)));
+  for (int i = 0; i < 4; ++i) {
+    uint64_t v = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    if constexpr (kTiny) v = f2_mul(v, f2(f, f));
+    uint64_t q = f2_mul(v, inv2);
+    q = f2_fma(f2_fma(q, ns2, v), inv2, q);
+    q = f2_fma(f2_fma(q, ns2, v), inv2, q);
+    if constexpr (kTiny) {
+      float a, b;
+      f2_split(q, a, b);
+      q = f2(fminf(fmaxf(a, -m), m), fminf(fmaxf(b, -m), m));
+    }
+    q = f2_add(q, round2);
+    float a, b;
+    f2_split(q, a, b);
+    c[2 * i] = __float_as_uint(a);
+    c[2 * i + 1] = __float_as_uint(b);
   }
+  uint2 o;
+  o.x = prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u);
+  o.y = prmt(prmt(c[4], c[5], 0x0040u), prmt(c[6], c[7], 0x0040u), 0x5410u);
+  if constexpr (kBits == 4) {  // low nibbles of two bytes into one byte
+    o.x &= 0x0f0f0f0fu;
+    o.y &= 0x0f0f0f0fu;
+    o.x = prmt(o.x | o.x >> 4, o.y | o.y >> 4, 0x6420u);
+  }
+  return o;
 }
 
 template <int kBits>
-__device__ __forceinline__ void kv_store8(uint8_t* dst, const uint32_t (&c)[8]) {
-  if constexpr (kBits == 8) {
-    uint2 o;
-    o.x = prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u);
-    o.y = prmt(prmt(c[4], c[5], 0x0040u), prmt(c[6], c[7], 0x0040u), 0x5410u);
+__device__ __forceinline__ void kv_store8(uint8_t* dst, const uint2& o) {
+  if constexpr (kBits == 8)
     *reinterpret_cast<uint2*>(dst) = o;
-  } else {
-    uint32_t o = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o |= (c[i] & 15u) << (4 * i);
-    *reinterpret_cast<uint32_t*>(dst) = o;
-  }
+  else
+    *reinterpret_cast<uint32_t*>(dst) = o.x;
 }
 
-template <int D, int kBits, bool kPaged>
+// kTokens: tokens of a warp, 32 (coalesced scales, one lookup of 32 places) or, for calls too small to
+// fill the GPU that way, one step of 512 / D.
+template <int D, int kBits, bool kPaged, int kTokens>
 __global__ void __launch_bounds__(256) fa_kv_write_kernel(const KvCopyParams p) {
-  constexpr int kLanes = D / 16;         // lanes of one row
-  constexpr int kRows = 32 / kLanes;     // rows the warp holds at once
-  constexpr int kSteps = 32 / kRows;     // ... of the 32 it takes
-  constexpr int kRow = D * kBits / 8;    // bytes of one row of codes
+  constexpr int kLanes = D / 16;           // lanes of one row
+  constexpr int kRows = 32 / kLanes;       // rows the warp holds at once
+  constexpr int kSteps = kTokens / kRows;  // ... of the ones it takes
+  constexpr int kU = kSteps < 4 ? kSteps : 4;  // steps in flight
+  constexpr int kRow = D * kBits / 8;      // bytes of one row of codes
   constexpr float m = kBits == 8 ? 127.f : 7.f;
   const KvMap& map = p.map;
-  if constexpr (kPaged) kv_check_cu(map);
   const int lane = threadIdx.x & 31;
   const long long unit = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int head = static_cast<int>(unit % map.Hkv);
   const long long rest = unit / map.Hkv;
   const bool is_v = rest & 1;
-  const long long tok0 = (rest >> 1) * 32;
+  const long long tok0 = (rest >> 1) * kTokens;
+  if constexpr (kPaged) kv_check_cu(map);
   if (tok0 >= map.N) return;
-  const uint16_t* x = is_v ? p.v : p.k;
   const long long stride = is_v ? p.v_stride : p.k_stride;
+  const uint16_t* x = (is_v ? p.v : p.k) + tok0 * stride + static_cast<long long>(head) * D;
   uint8_t* codes = is_v ? p.v_codes : p.k_codes;
   float* scales = is_v ? p.v_scale : p.k_scale;
+  const int left = static_cast<int>(min(static_cast<long long>(kTokens), map.N - tok0));
 
-  int page, row;  // of token tok0 + lane
-  kv_locate<kPaged>(map, static_cast<int>(min(tok0 + lane, static_cast<long long>(map.N))), page,
-                    row);
-  float my_scale = 0.f;
   const int l = lane % kLanes;
-#pragma unroll 1
-  for (int s0 = 0; s0 < kSteps; s0 += 4) {
-    uint4 w[4][2];
+  uint4 w[kU][2];
+  auto load = [&](int s0) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kU; ++u) {
       const int r = (s0 + u) * kRows + lane / kLanes;
       w[u][0] = w[u][1] = make_uint4(0, 0, 0, 0);
-      if (__shfl_sync(0xffffffffu, page, r) >= 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(x + (tok0 + r) * stride +
-                                                          static_cast<long long>(head) * D);
+      if (r < left) {
+        const uint4* src = reinterpret_cast<const uint4*>(x + r * stride);
         w[u][0] = __ldg(src + l);
         w[u][1] = __ldg(src + l + kLanes);
       }
     }
+  };
+  load(0);  // (on its way while the places are looked up)
+  int page = -1, row = 0;  // of token tok0 + lane
+  if (lane < left) kv_locate<kPaged>(map, static_cast<int>(tok0) + lane, page, row);
+  float my_scale = 0.f;
+#pragma unroll 1
+  for (int s0 = 0; s0 < kSteps; s0 += kU) {
+    if (s0 > 0) load(s0);
+    // lane l < kU of a row's lanes takes the scale of step s0 + l
+    uint32_t top = 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = (s0 + u) * kRows + lane / kLanes;
-      const int pg = __shfl_sync(0xffffffffu, page, r);
-      const int rw = __shfl_sync(0xffffffffu, row, r);
+    for (int u = 0; u < kU; ++u) {
       // |bf16| as 16-bit integers keeps the order (infinity 0x7f80, NaN above)
       constexpr uint32_t kAbs = 0x7fff7fffu;
-      uint32_t a = max_u16x2(max_u16x2(max_u16x2(w[u][0].x & kAbs, w[u][0].y & kAbs),
-                                       max_u16x2(w[u][0].z & kAbs, w[u][0].w & kAbs)),
-                             max_u16x2(max_u16x2(w[u][1].x & kAbs, w[u][1].y & kAbs),
-                                       max_u16x2(w[u][1].z & kAbs, w[u][1].w & kAbs)));
+      uint32_t a = __vmaxu2(__vmaxu2(__vmaxu2(w[u][0].x & kAbs, w[u][0].y & kAbs),
+                                     __vmaxu2(w[u][0].z & kAbs, w[u][0].w & kAbs)),
+                            __vmaxu2(__vmaxu2(w[u][1].x & kAbs, w[u][1].y & kAbs),
+                                     __vmaxu2(w[u][1].z & kAbs, w[u][1].w & kAbs)));
 #pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) a = max_u16x2(a, __shfl_xor_sync(0xffffffffu, a, o));
-      a = max(a & 0xffffu, a >> 16);
-      const bool finite = a < 0x7f80u;
-      const float scale = finite ? __fdiv_rn(__uint_as_float(a << 16), m) : __int_as_float(0x7fc00000);
-      // below this 1 / scale nears the end of the fp32 range: exact divisions
-      const bool tiny = scale < 1e-30f;
-      const bool zero = a == 0 || !finite;
-      const float inv = (zero || tiny) ? 0.f : __frcp_rn(scale);
-      uint32_t c0[8], c1[8];
-      float d = 0.f;
-      kv_codes8(w[u][0], zero ? 0.f : inv, c0, d);
-      kv_codes8(w[u][1], zero ? 0.f : inv, c1, d);
-      if (!zero && (tiny || d > 0.5f - 0x1p-14f)) {
-        kv_codes8_exact<kBits>(w[u][0], scale, c0);
-        kv_codes8_exact<kBits>(w[u][1], scale, c1);
-      }
-      if (!finite) {
+      for (int o = 1; o < kLanes; o <<= 1) a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, o));
+      if (l % kU == u) top = max(a & 0xffffu, a >> 16);
+    }
+    const bool finite = top < 0x7f80u;
+    const float scale = finite ? __fdiv_rn(__uint_as_float(top << 16), m) : __int_as_float(0x7fc00000);
+    const bool tiny = scale < 0x1p-90f && top != 0;
+    const bool any_tiny = __any_sync(0xffffffffu, tiny);
+    const float f = tiny ? 0x1p96f : 1.f;
+    const float base = scale * f;
+    // 1 / scale = 0 makes every code 0
+    const float inv = (top == 0 || !finite) ? 0.f : __frcp_rn(base);
+    const float from = __shfl_sync(0xffffffffu, scale, lane % kRows * kLanes + lane / kRows % kU);
+    if (lane / kRows / kU == s0 / kU) my_scale = from;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c0[i] = c1[i] = 0;
+    for (int u = 0; u < kU; ++u) {
+      const int r = (s0 + u) * kRows + lane / kLanes;
+      const int pg = __shfl_sync(0xffffffffu, page, r & 31);
+      const int rw = __shfl_sync(0xffffffffu, row, r & 31);
+      const float inv_u = __shfl_sync(0xffffffffu, inv, lane / kLanes * kLanes + u);
+      const float ns_u = -__shfl_sync(0xffffffffu, base, lane / kLanes * kLanes + u);
+      uint2 c0, c1;
+      if (!any_tiny) {
+        c0 = kv_codes8<kBits, false>(w[u][0], inv_u, ns_u, 1.f);
+        c1 = kv_codes8<kBits, false>(w[u][1], inv_u, ns_u, 1.f);
+      } else {
+        const float f_u = __shfl_sync(0xffffffffu, f, lane / kLanes * kLanes + u);
+        c0 = kv_codes8<kBits, true>(w[u][0], inv_u, ns_u, f_u);
+        c1 = kv_codes8<kBits, true>(w[u][1], inv_u, ns_u, f_u);
       }
-      const float s_lane = __shfl_sync(0xffffffffu, scale, (lane % kRows) * kLanes);
-      if (lane / kRows == s0 + u) my_scale = s_lane;
+      if (inv_u == 0.f) c0 = c1 = make_uint2(0, 0);
       if (pg >= 0) {
         uint8_t* dst = codes + ((static_cast<size_t>(pg) * map.page_size + rw) * map.Hkv + head) * kRow;
         kv_store8<kBits>(dst + kBits * l, c0);
@@ -252,11 +274,11 @@ __device__ __forceinline__ uint4 kv_values8(const uint8_t* src, float scale) {
   return o;
 }
 
-template <int D, int kBits, bool kPaged>
+template <int D, int kBits, bool kPaged, int kTokens>
 __global__ void __launch_bounds__(256) fa_kv_read_kernel(const KvCopyParams p) {
   constexpr int kLanes = D / 16;
   constexpr int kRows = 32 / kLanes;
-  constexpr int kSteps = 32 / kRows;
+  constexpr int kSteps = kTokens / kRows;
   constexpr int kRow = D * kBits / 8;
   const KvMap& map = p.map;
   if constexpr (kPaged) kv_check_cu(map);
@@ -265,15 +287,15 @@ __global__ void __launch_bounds__(256) fa_kv_read_kernel(const KvCopyParams p) {
   const int head = static_cast<int>(unit % map.Hkv);
   const long long rest = unit / map.Hkv;
   const bool is_v = rest & 1;
-  const long long tok0 = (rest >> 1) * 32;
+  const long long tok0 = (rest >> 1) * kTokens;
   if (tok0 >= map.N) return;
+  const int left = static_cast<int>(min(static_cast<long long>(kTokens), map.N - tok0));
   const uint8_t* codes = is_v ? p.v_codes : p.k_codes;
   const float* scales = is_v ? p.v_scale : p.k_scale;
   uint16_t* out = is_v ? p.v_out : p.k_out;
 
-  int page, row;
-  kv_locate<kPaged>(map, static_cast<int>(min(tok0 + lane, static_cast<long long>(map.N))), page,
-                    row);
+  int page = -1, row = 0;
+  if (lane < left) kv_locate<kPaged>(map, static_cast<int>(tok0) + lane, page, row);
   const float my_scale =
       page >= 0 ? scales[(static_cast<size_t>(page) * map.Hkv + head) * map.page_size + row] : 0.f;
   const int l = lane % kLanes;
