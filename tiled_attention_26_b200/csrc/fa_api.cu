@@ -535,7 +535,7 @@ int shared_prefix_splits(int B, int Hq, int Hkv, long long max_keys) {
     const long long ctas = Hkv * ((R + 7) / 8);
     return static_cast<int>(std::min(tiles, std::max(1ll, 3 * kSms / ctas)));
   }
-  const long long base = static_cast<long long>(Hkv) * ((R + 127) / 128);
+  const long long base = static_cast<long long>(Hkv) * (R <= 128 ? 1 : (R + 255) / 256);
   int best = 1;
   long long best_cost = -1;
   for (int s = 1; s <= kSms && s <= tiles; ++s) {
@@ -555,17 +555,27 @@ int shared_own_splits(int B, int Hq, int Hkv, long long max_keys) {
   return static_cast<int>(std::max(1ll, std::min((3 * kSms + ctas - 1) / ctas, (max_keys + 127) / 128)));
 }
 
-std::atomic<uint64_t> g_attr_shared[4];
+std::atomic<uint64_t> g_attr_shared[8];
+std::atomic<int> g_shared_regs[8] = {};  // registers per thread of each variant, 0 = not read
 
-template <int D, int kBits>
+template <int D, int kBits, bool kStream>
 int launch_shared_prefix(const CodeMaps& maps, const fa::SharedParams& p, cudaStream_t stream) {
-  using C = fa::SharedCfg<D, kBits>;
+  using C = fa::SharedCfg<D, kBits, kStream>;
   const long long grid = static_cast<long long>(p.Hkv) * p.row_blocks * p.splits;
   if (grid > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
-  auto kernel = fa::fa_shared_prefix_kernel<D, kBits>;
-  constexpr int variant = (D == 128 ? 2 : 0) + (kBits == 4 ? 1 : 0);
+  auto kernel = fa::fa_shared_prefix_kernel<D, kBits, kStream>;
+  constexpr int variant = (D == 128 ? 4 : 0) + (kBits == 4 ? 2 : 0) + (kStream ? 1 : 0);
   const int rc = ensure_smem_attr(kernel, C::kSmemBytes, g_attr_shared[variant]);
   if (rc != FA_OK) return rc;
+  // setmaxnreg redistributes the launch's registers; it only completes if they cover the split
+  int regs = g_shared_regs[variant].load(std::memory_order_acquire);
+  if (regs == 0) {
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess) return FA_ERR_CUDA;
+    regs = attr.numRegs;
+    g_shared_regs[variant].store(regs, std::memory_order_release);
+  }
+  if (regs < C::kLaunchRegs) return FA_ERR_UNSUPPORTED;
   return launch(kernel, dim3(static_cast<unsigned>(grid)), C::kThreads, C::kSmemBytes, true, stream,
                 maps.k, maps.v, p);
 }
@@ -591,8 +601,10 @@ int launch_shared(const fa::DecodeParams& own, const fa::SharedParams& sp, void*
     pre.o_part = sp.o_part;
     pre.lse_part = sp.lse_part;
     rc = launch_split<D, true, kBits>(maps, pre, true, stream);
+  } else if (sp.R <= 128) {
+    rc = launch_shared_prefix<D, kBits, true>(maps, sp, stream);
   } else {
-    rc = launch_shared_prefix<D, kBits>(maps, sp, stream);
+    rc = launch_shared_prefix<D, kBits, false>(maps, sp, stream);
   }
   if (rc != FA_OK) return rc;
   return launch_combine<D>(own, own.splits + sp.splits, o, lse, stream);
@@ -772,7 +784,7 @@ int decode_shared(int bits, const void* q, const void* k, const void* v, const f
   sp.Hkv = Hkv;
   sp.G = Hq / Hkv;
   sp.R = B * sp.G;
-  sp.row_blocks = (sp.R + 127) / 128;
+  sp.row_blocks = sp.R <= 128 ? 1 : (sp.R + 255) / 256;
   sp.splits = prefix;
   sp.max_pages = max_prefix_pages;
   sp.num_pages = num_pages;
