@@ -100,6 +100,30 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_CALLS = ["fa_kv_quantize_int8", "fa_kv_quantize_int4", "fa_kv_dequantize_int8",
+          "fa_kv_dequantize_int4", "fa_kv_append_int8_paged", "fa_kv_append_int4_paged",
+          "fa_kv_gather_int8_paged", "fa_kv_gather_int4_paged", "fa_decode_int8_shared",
+          "fa_decode_int4_shared", "fa_decode_shared_workspace_bytes"]
+_direct_calls = None
+
+
+def _direct():
+    """The direct calls of csrc/torch_calls.cpp: each makes the plain case of its entry point's call,
+    or returns None and leaves it to the code here."""
+    global _direct_calls
+    if _direct_calls is None:
+        L = lib()
+        import torch  # noqa: F401  (its libraries must be loaded first)
+        try:
+            from . import _torch_calls
+        except ImportError as e:
+            raise RuntimeError("_torch_calls.so is not built; run "
+                               "`python tiled_attention_26_b200/build.py`") from e
+        _torch_calls.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _CALLS))
+        _direct_calls = _torch_calls
+    return _direct_calls
+
+
 def fa_status_string(status: int) -> str:
     return lib().fa_status_string(int(status)).decode()
 
@@ -376,6 +400,12 @@ def _code_type(bits, D):
 
 
 def _kv_quantize(bits, k, v, k_codes, v_codes, k_scale, v_scale, stream):
+    if stream is None:
+        r = _direct().kv_quantize(bits, k, v, k_codes, v_codes, k_scale, v_scale)
+        if r is not None:
+            if r[0] != 0:
+                raise FaError(r[0], f"fa_kv_quantize_int{bits}")
+            return r[1:]
     import torch
     name = f"fa_kv_quantize_int{bits}"
     if k.dim() != 4:
@@ -410,6 +440,12 @@ def fa_kv_quantize_int4(k, v, k_codes=None, v_codes=None, k_scale=None, v_scale=
 
 
 def _kv_dequantize(bits, k_codes, v_codes, k_scale, v_scale, k, v, stream):
+    if stream is None:
+        r = _direct().kv_dequantize(bits, k_codes, v_codes, k_scale, v_scale, k, v)
+        if r is not None:
+            if r[0] != 0:
+                raise FaError(r[0], f"fa_kv_dequantize_int{bits}")
+            return r[1:]
     import torch
     name = f"fa_kv_dequantize_int{bits}"
     if k_codes.dim() != 4:
@@ -486,6 +522,13 @@ def _token_rows(t, name, Hkv, D, dev):
 
 def _kv_append(bits, k, v, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, positions,
                cu_tokens, stream):
+    if stream is None:
+        rc = _direct().kv_append(bits, k, v, k_pages, v_pages, k_scale_pages, v_scale_pages,
+                                 block_table, positions, cu_tokens)
+        if rc is not None:
+            if rc != 0:
+                raise FaError(rc, f"fa_kv_append_int{bits}_paged")
+            return
     import torch
     name = f"fa_kv_append_int{bits}_paged"
     dev, D = k.device, k.shape[-1]
@@ -531,6 +574,13 @@ def fa_kv_append_int4_paged(k, v, k_pages, v_pages, k_scale_pages, v_scale_pages
 
 def _kv_gather(bits, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table, num_tokens,
                positions, cu_tokens, k, v, stream):
+    if stream is None:
+        r = _direct().kv_gather(bits, k_pages, v_pages, k_scale_pages, v_scale_pages, block_table,
+                                num_tokens, positions, cu_tokens, k, v)
+        if r is not None:
+            if r[0] != 0:
+                raise FaError(r[0], f"fa_kv_gather_int{bits}_paged")
+            return r[1:]
     import torch
     name = f"fa_kv_gather_int{bits}_paged"
     dev = k_pages.device
@@ -584,6 +634,14 @@ def fa_decode_shared_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, max_pref
 def _decode_shared(bits, q, k_pages, v_pages, k_scale_pages, v_scale_pages, prefix_table,
                    prefix_len, block_table, seqlens, num_splits, scale, o, lse, workspace,
                    return_lse, stream):
+    if stream is None:
+        r = _direct().decode_shared(bits, q, k_pages, v_pages, k_scale_pages, v_scale_pages,
+                                    prefix_table, prefix_len, block_table, seqlens, num_splits, scale,
+                                    o, lse, workspace, return_lse)
+        if r is not None:
+            if r[0] != 0:
+                raise FaError(r[0], f"fa_decode_int{bits}_shared")
+            return r[1:]
     import torch
     name = f"fa_decode_int{bits}_shared"
     if q.dim() != 4 or q.shape[1] != 1:

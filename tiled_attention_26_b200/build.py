@@ -1,14 +1,18 @@
-"""Build ``libfa.so`` (the C-ABI attention library) for sm_100a with nvcc, in-tree."""
+"""Build ``libfa.so`` (the C-ABI attention library) for sm_100a with nvcc, and ``_torch_calls.so`` (its
+direct calls for torch tensors) with the host compiler, in-tree."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfa.so")
+CALLS = os.path.join(HERE, "_torch_calls.so")
+CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
 SOURCES = [os.path.join(CSRC, "fa_api.cu")]
 DEPS = SOURCES + sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")) + [
     os.path.join(ROOT, "include", "fa.h")]
@@ -25,9 +29,31 @@ def nvcc() -> str:
     return "nvcc"
 
 
+def _stale(out: str, deps) -> bool:
+    return not os.path.exists(out) or os.path.getmtime(out) < max(os.path.getmtime(p) for p in deps)
+
+
+def build_calls(force: bool = False) -> str:
+    if not force and not _stale(CALLS, [CALLS_SOURCE, os.path.join(ROOT, "include", "fa.h")]):
+        return CALLS
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for inc in (os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]):
+        cmd += ["-isystem", inc]
+    cmd += [CALLS_SOURCE, "-o", CALLS + ".tmp", "-L" + os.path.join(t, "lib"), "-ltorch", "-ltorch_cpu",
+            "-ltorch_python", "-lc10", "-lc10_cuda"]
+    subprocess.run(cmd, check=True)
+    os.replace(CALLS + ".tmp", CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    newest = max(os.path.getmtime(p) for p in DEPS)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
+    build_calls(force)
+    if not force and not _stale(LIB, DEPS):
         return LIB
     cmd = [nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose else []) + [
         "-I", os.path.join(ROOT, "include")] + SOURCES + ["-o", LIB + ".tmp"]

@@ -548,11 +548,15 @@ int shared_prefix_splits(int B, int Hq, int Hkv, long long max_keys) {
   return best;
 }
 
-// Splits of the sequences' own keys where the caller leaves the choice to the library: as many as
-// fill the SMs (3 CTAs each), no more than there are 128-key stages.
-int shared_own_splits(int B, int Hq, int Hkv, long long max_keys) {
+// Splits of the sequences' own keys where the caller leaves the choice to the library: pieces of 1024
+// keys (INT4, whose stages take twice as long: 512), as long as three CTAs per SM hold them.  The prefix's
+// kernel runs beside or right behind this one on the same SMs, so fewer, longer CTAs beat a full
+// GPU: B200, 12 sequences x 232 heads of 64 dims, 256 own keys, 1 / 2 / 4 splits 33 / 39 / 43 us,
+// 8 x 32 heads, 1024 keys 20.5 / 22.5 / 22.6 us; INT4, 13 x 28 heads, 777 keys 32.8 / 28.6 / 28.7 us.
+int shared_own_splits(int bits, int B, int Hq, int Hkv, long long max_keys) {
   const long long ctas = static_cast<long long>(B) * Hkv * ((Hq / Hkv + 7) / 8);
-  return static_cast<int>(std::max(1ll, std::min((3 * kSms + ctas - 1) / ctas, (max_keys + 127) / 128)));
+  const long long keys = bits == 8 ? 1024 : 512;
+  return static_cast<int>(std::max(1ll, std::min(3 * kSms / ctas, (max_keys + keys - 1) / keys)));
 }
 
 std::atomic<uint64_t> g_attr_shared[8];
@@ -723,13 +727,13 @@ int kv_paged(const void* k, const void* v, int64_t k_stride, int64_t v_stride, c
 }
 
 // Sizes of a shared decode call that the workspace depends on; false if they are not valid.
-bool shared_splits(int B, int Hq, int Hkv, int D, long long max_prefix, long long max_own,
+bool shared_splits(int bits, int B, int Hq, int Hkv, int D, long long max_prefix, long long max_own,
                    int num_splits, int* own, int* prefix) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0 || max_prefix <= 0 || max_own <= 0 ||
       num_splits < 0)
     return false;
   if (static_cast<long long>(B) * Hq > 0x7fffffffLL) return false;
-  *own = num_splits > 0 ? num_splits : shared_own_splits(B, Hq, Hkv, max_own);
+  *own = num_splits > 0 ? num_splits : shared_own_splits(bits, B, Hq, Hkv, max_own);
   *prefix = shared_prefix_splits(B, Hq, Hkv, max_prefix);
   return *own <= 65535;
 }
@@ -750,7 +754,7 @@ int decode_shared(int bits, const void* q, const void* k, const void* v, const f
   const long long max_own = static_cast<long long>(max_pages) << shift;
   if (max_prefix > (1ll << 30) || max_own > (1ll << 30)) return FA_ERR_INVALID_ARG;
   int own = 0, prefix = 0;
-  if (!shared_splits(B, Hq, Hkv, D, max_prefix, max_own, num_splits, &own, &prefix))
+  if (!shared_splits(bits, B, Hq, Hkv, D, max_prefix, max_own, num_splits, &own, &prefix))
     return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * ((Hq / Hkv + 7) / 8) > 65535) return FA_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
@@ -1038,7 +1042,8 @@ int fa_kv_gather_int4_paged(const uint8_t* k_pages, const uint8_t* v_pages, cons
 size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int D, int max_prefix_len,
                                         int max_seqlen, int num_splits) {
   int own = 0, prefix = 0;
-  if (!shared_splits(B, Hq, Hkv, D, max_prefix_len, max_seqlen, num_splits, &own, &prefix)) return 0;
+  // (INT4's splits: never fewer than INT8's)
+  if (!shared_splits(4, B, Hq, Hkv, D, max_prefix_len, max_seqlen, num_splits, &own, &prefix)) return 0;
   return decode_ws_layout(B, Hq, D, own + prefix, nullptr);
 }
 
