@@ -99,11 +99,12 @@ __device__ __forceinline__ void kv_check_cu(const KvMap& m) {
 }
 
 // The codes of the 8 bf16 values in x as 8 bytes (INT8) or nibbles (INT4): rint(fl32(x / scale)),
-// with inv = 1 / scale rounded and nscale = -scale.  fl32(x / scale) comes from inv by two steps of
-// q + (x - q scale) inv: after the first q is off by less than a unit in the last place, after the
-// second it is the rounded quotient (P. Markstein, "Computation of elementary functions on the IBM
-// RISC System/6000 processor", 1990).  Quotients that fall on or near a half are common - x = max / 2
-// is one - so every value takes both.
+// with inv = 1 / scale rounded and nscale = -scale.  The quotient comes from inv by one step of
+// q + (x - q scale) inv (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990).  That leaves it off the rounded quotient by a unit in the last place at
+// most; for scales that are a bf16 over m it rounds to the same code always (all pairs of mantissas and
+// exponents, which is what the outcome depends on, are a test), x * inv alone does not: quotients on or
+// next to a half are common, x = max / 2 is one.
 // kTiny: x is multiplied by f first, as the scale was.  2^96 keeps the residuals of rows with scales
 // below 2^-90 in the normal range (and changes no quotient); codes are clamped, for a scale below the
 // normal range can be far enough off max|x| / m for the quotient to pass m.
@@ -119,7 +120,6 @@ __device__ __forceinline__ uint2 kv_codes8(const uint4& x, float inv, float nsca
     uint64_t v = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     if constexpr (kTiny) v = f2_mul(v, f2(f, f));
     uint64_t q = f2_mul(v, inv2);
-    q = f2_fma(f2_fma(q, ns2, v), inv2, q);
     q = f2_fma(f2_fma(q, ns2, v), inv2, q);
     if constexpr (kTiny) {
       float a, b;
