@@ -278,18 +278,22 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
     // rather than the last.  CTA rank r takes the sequence of length rank r (ties by index);
     // each thread ranks one sequence (up to kDecodeRankMaxB sequences; larger batches keep their
     // order).  Lengths are clamped as below, so a bad one cannot break the permutation.
-    __shared__ int s_len[kDecodeRankMaxB];
+    __shared__ __align__(16) int s_len[kDecodeRankMaxB];
     __shared__ int s_b;
     if (p.B <= kDecodeRankMaxB) {
       const int cap = p.max_pages << p.page_shift;
-      if (threadIdx.x < p.B) s_len[threadIdx.x] = max(0, min(p.seqlens[threadIdx.x], cap));
+      if (threadIdx.x < kDecodeRankMaxB)  // (-1: behind every sequence)
+        s_len[threadIdx.x] = threadIdx.x < p.B ? max(0, min(p.seqlens[threadIdx.x], cap)) : -1;
       __syncthreads();
       if (threadIdx.x < p.B) {
         const int me = threadIdx.x, lme = s_len[me];
         int rank = 0;
-        for (int x = 0; x < p.B; ++x) {
-          const int lx = s_len[x];
-          rank += (lx > lme || (lx == lme && x < me)) ? 1 : 0;
+        for (int x = 0; x < p.B; x += 4) {
+          const int4 l4 = *reinterpret_cast<const int4*>(s_len + x);
+          rank += (l4.x > lme || (l4.x == lme && x < me)) ? 1 : 0;
+          rank += (l4.y > lme || (l4.y == lme && x + 1 < me)) ? 1 : 0;
+          rank += (l4.z > lme || (l4.z == lme && x + 2 < me)) ? 1 : 0;
+          rank += (l4.w > lme || (l4.w == lme && x + 3 < me)) ? 1 : 0;
         }
         if (rank == b) s_b = me;
       }
@@ -373,38 +377,40 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
     int issued = 0;
     for (int i = 0; i < n_stages; ++i) {
       const int s = i % C::kStages;
-      if (i >= C::kStages && !mbar_wait(bar_empty(s), ((i / C::kStages) - 1) & 1, ctl)) break;
+      const bool free = i < C::kStages || mbar_wait(bar_empty(s), ((i / C::kStages) - 1) & 1, ctl);
+      if (!__all_sync(0xffffffffu, free)) break;
       const int t0 = t_begin + C::kT * i;
       const uint32_t ks_dst = sb + C::kScaleOff + s * 2 * C::kT * 4;
       const uint32_t vs_dst = ks_dst + C::kT * 4;
       if (bulk_scales) {
-        // One thread issues everything: the K/V code boxes and, beside each, its keys' scales
-        // as one bulk copy (a page's scales are contiguous; so are a row segment's).  Keys past
-        // the split's end get real scales of the same page or row; the consumers mask them.
-        if (lane == 0) {
-          const uint32_t seg =
-              kPaged ? C::kT * 4 : static_cast<uint32_t>(min(C::kT, p.Skv - t0)) * 4;
-          mbar_arrive_expect_tx(bar_full(s), C::kStageBytes + 2 * seg);
-          const uint32_t kt = sb + s * C::kStageBytes, vt = kt + C::kTile;
-          for (int t = t0; t < t0 + C::kT; t += box_t) {
-            const uint32_t off = (t - t0) * C::kRow;  // box_t divides kT: stays inside the tile
+        // The K/V code boxes and, beside each, its keys' scales as one bulk copy (a page's scales are
+        // contiguous; so are a row segment's).  Lane 4 i + k issues copy k (K codes, V codes, K
+        // scales, V scales) of box i: a stage of 16-key pages takes 32 copies, three times as long from
+        // one lane as computing on the stage.  Keys past the split's end get real scales of the same
+        // page or row; the consumers mask them.
+        const uint32_t seg =
+            kPaged ? C::kT * 4 : static_cast<uint32_t>(min(C::kT, p.Skv - t0)) * 4;
+        if (lane == 0) mbar_arrive_expect_tx(bar_full(s), C::kStageBytes + 2 * seg);
+        __syncwarp();
+        const int kind = lane & 3, at = (lane >> 2) * box_t;  // box_t >= 16: 8 boxes at most
+        if (at < C::kT) {
+          const bool is_v = kind & 1;
+          if (kind < 2) {
+            const uint32_t dst = sb + s * C::kStageBytes + (is_v ? C::kTile : 0) + at * C::kRow;
+            // a box past the split's last key reads the split's last page
+            const int c2 = kPaged ? (t0 + at) & pmask : t0 + at;
+            const int c3 = kPaged ? page_of(min(t0 + at, t_end - 1)) : b;
+            tma_load_4d_policy(dst, is_v ? &tm_v : &tm_k, bar_full(s), 0, kvh, c2, c3, stream_pol);
+          } else {
+            const uint32_t dst = (is_v ? vs_dst : ks_dst) + 4 * at;
+            const float* src = is_v ? p.v_scale : p.k_scale;
             if constexpr (kPaged) {
-              // a box past the split's last key reads the split's last page
-              const int pg = page_of(min(t, t_end - 1));
-              const int r0 = t & pmask;
-              tma_load_4d_policy(kt + off, &tm_k, bar_full(s), 0, kvh, r0, pg, stream_pol);
-              tma_load_4d_policy(vt + off, &tm_v, bar_full(s), 0, kvh, r0, pg, stream_pol);
-              const size_t idx = ((static_cast<size_t>(pg) * p.Hkv + kvh) << p.page_shift) + r0;
-              bulk_g2s(ks_dst + 4 * (t - t0), p.k_scale + idx, 4 * box_t, bar_full(s));
-              bulk_g2s(vs_dst + 4 * (t - t0), p.v_scale + idx, 4 * box_t, bar_full(s));
+              const int pg = page_of(min(t0 + at, t_end - 1));
+              src += ((static_cast<size_t>(pg) * p.Hkv + kvh) << p.page_shift) + ((t0 + at) & pmask);
+              bulk_g2s(dst, src, 4 * box_t, bar_full(s));
             } else {
-              tma_load_4d_policy(kt + off, &tm_k, bar_full(s), 0, kvh, t, b, stream_pol);
-              tma_load_4d_policy(vt + off, &tm_v, bar_full(s), 0, kvh, t, b, stream_pol);
+              bulk_g2s(dst, (is_v ? vs_row : ks_row) + t0, seg, bar_full(s));
             }
-          }
-          if constexpr (!kPaged) {
-            bulk_g2s(ks_dst, ks_row + t0, seg, bar_full(s));
-            bulk_g2s(vs_dst, vs_row + t0, seg, bar_full(s));
           }
         }
         __syncwarp();
@@ -471,12 +477,18 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
     const bool hv = g < nheads;
     const uint16_t* qrow = p.q + row_of(hv ? g : 0) * D;
     float amax = 0.f;
+    uint4 raw[QD / 8];
+#pragma unroll
+    for (int i = 0; i < QD / 8; ++i)
+      raw[i] = hv ? __ldg(reinterpret_cast<const uint4*>(qrow + QD * c) + i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int dim = kBits == 8 ? 4 * s + e : 8 * (s >> 1) + 2 * (s & 1) + (e >> 1) + 4 * (e & 1);
-        qv[s][e] = hv ? bf16_bits_to_float(qrow[QD * c + dim]) : 0.f;
+        const uint4& v = raw[dim / 8];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        qv[s][e] = bf16_bits_to_float(static_cast<uint16_t>(w[dim / 2 % 4] >> (16 * (dim & 1))));
         amax = fmaxf(amax, fabsf(qv[s][e]));
       }
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
@@ -724,22 +736,29 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
     ow[(2 * c + 1) * D + d0 + 1] = oacc[mt][3] * unscale_hi;
   }
   named_bar_sync(1, 128);
-  for (int idx = threadIdx.x; idx < nheads * D; idx += 128) {
-    const int h = idx / D, d = idx % D;
+  for (int idx = threadIdx.x; idx < nheads * (D / 4); idx += 128) {  // 4 dims
+    const int h = idx / (D / 4), d = idx % (D / 4) * 4;
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < 4; ++w) M = fmaxf(M, sm_m[w * 8 + h]);
     // a sum of 0 means no key; a NaN among the scales (a row written from a NaN) stays one
-    float L = 0.f, acc = 0.f;
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const float mw = sm_m[w * 8 + h];
       const float f = (mw == -INFINITY) ? 0.f : ex2(mw - M);
       L += f * sm_l[w * 8 + h];
-      acc += f * sm_o[(w * 8 + h) * D + d];
+      const float4 o = *reinterpret_cast<const float4*>(sm_o + (w * 8 + h) * D + d);
+      acc.x += f * o.x;
+      acc.y += f * o.y;
+      acc.z += f * o.z;
+      acc.w += f * o.w;
     }
     const size_t row = static_cast<size_t>(split) * p.rows + row_of(h);
-    p.o_part[row * D + d] = (L == 0.f) ? 0.f : acc / L;
+    *reinterpret_cast<float4*>(p.o_part + row * D + d) =
+        (L == 0.f) ? make_float4(0.f, 0.f, 0.f, 0.f)
+                   : make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L);
     if (d == 0) p.lse_part[row] = (L == 0.f) ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
   }
 }

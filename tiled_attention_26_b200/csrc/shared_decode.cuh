@@ -240,6 +240,31 @@ __global__ void __launch_bounds__(512, 1)
     tmem_alloc(smem_u32(tmem_holder), C::kTmemCols);
     tmem_relinquish();
   }
+  // What the warps read first is on its way before the barrier: the producer's and the scale warp's
+  // page-table entries of the first tile, and the query rows (a warp fetches the 32 rows of its threads,
+  // D / 8 lanes a row; streams: both warpgroups the same rows).
+  const int box_t = min(128, 1 << p.page_shift), boxes = 128 / box_t;  // keys of a TMA box, boxes of a tile
+  auto entry_at = [&](int j) -> int {  // of this lane's box, or of its 4 keys
+    const int t = t_begin + 128 * j + lane * (warp == 12 ? box_t : 4);
+    return j < nt && t < t_end && (warp != 12 || lane < boxes) ? __ldg(p.table + (t >> p.page_shift)) : 0;
+  };
+  int entry = 0;
+  constexpr int kQLanes = D / 8, kQRows = 32 / kQLanes, kQSteps = 32 / kQRows;
+  uint4 q_raw[kQSteps];
+  const int R = (kStream || warp >= 8 ? 0 : (warp >> 2) * 128) + (threadIdx.x & 127);  // row of the CTA
+  if (warp == 12 || warp == 14) {
+    entry = entry_at(0);
+  } else if (warp < 8) {
+    const int mine = static_cast<int>(out_row(min(R, live - 1)));
+#pragma unroll
+    for (int i = 0; i < kQSteps; ++i) {
+      const int row = i * kQRows + lane / kQLanes;
+      const size_t from = __shfl_sync(0xffffffffu, mine, row);
+      q_raw[i] = make_uint4(0, 0, 0, 0);
+      if ((R & ~31) + row < live)
+        q_raw[i] = __ldg(reinterpret_cast<const uint4*>(p.q + from * D) + lane % kQLanes);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -259,16 +284,10 @@ __global__ void __launch_bounds__(512, 1)
       // ================= TMA producer =================
       // lane i < boxes copies box i of each tile (a page, or 128 keys of a larger one); boxes past
       // the last key are skipped: the codes left there are finite and their scales count as 0
-      const int box_t = min(128, 1 << p.page_shift);
-      const int boxes = 128 / box_t;
       const int pmask = (1 << p.page_shift) - 1;
       const uint32_t box_bytes = static_cast<uint32_t>(box_t) * C::kRow;
       const uint64_t pol = l2_evict_first_policy();
-      auto entry_at = [&](int j) -> int {
-        const int t = t_begin + 128 * j + lane * box_t;
-        return lane < boxes && j < nt && t < t_end ? __ldg(p.table + (t >> p.page_shift)) : 0;
-      };
-      int entry = entry_at(0), issued = 0;
+      int issued = 0;
       bool ok = true;
       for (int j = 0; j < nt && ok; ++j) {
         const int next = entry_at(j + 1);
@@ -316,10 +335,6 @@ __global__ void __launch_bounds__(512, 1)
       // k_scale as it is, v_scale times 2^E; keys past the prefix count 0.  Table entries are read two
       // tiles ahead, scales one ahead.
       const int pmask = (1 << p.page_shift) - 1;
-      auto entry_at = [&](int j) -> int {
-        const int t = t_begin + 128 * j + 4 * lane;
-        return j < nt && t < t_end ? __ldg(p.table + (t >> p.page_shift)) : 0;
-      };
       auto scales_at = [&](int j, int entry, float4& ks, float4& vs) {
         const int t = t_begin + 128 * j + 4 * lane;
         ks = vs = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -331,8 +346,8 @@ __global__ void __launch_bounds__(512, 1)
         }
       };
       float4 ks, vs, ks_next, vs_next;
-      scales_at(0, entry_at(0), ks, vs);
-      int entry = entry_at(1);
+      scales_at(0, entry, ks, vs);
+      entry = entry_at(1);
       constexpr int kUnset = 1 << 20;
       int e0 = kUnset, e1 = kUnset;  // exponents of the accumulators of this tile and of the next
       for (int j = 0; j < nt; ++j) {
@@ -496,34 +511,22 @@ __global__ void __launch_bounds__(512, 1)
     // ================= Q, softmax, epilogue: thread r = query row r of S tile t =================
     const int t = warp >> 2;
     const int r = threadIdx.x & 127;
-    const int R = (kStream ? 0 : t * 128) + r;  // row of the CTA
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     const uint32_t colS = t ? C::colS(1) : C::colS(0);
     const uint32_t colO = t ? C::colO(1) : C::colO(0);
     const bool warp_live = (R & ~31) < live;  // a warp of padding rows only keeps the barriers
     const int first = kStream ? t : 0, step = kStream ? 2 : 1;
 
-    // Q: a warp fetches the 32 rows of its threads, D / 8 lanes a row (streams: both warpgroups fetch
-    // the same rows and lay out half of them).
-    constexpr int kQLanes = D / 8, kQRows = 32 / kQLanes, kQSteps = 32 / kQRows;
-    const int my_row = static_cast<int>(out_row(min(R, live - 1)));
     float sc = 0.f;  // of row R: score units of log2, undoing the row's power of two
 #pragma unroll 1  // (short code: it runs once, from a cold instruction cache)
     for (int i0 = 0; i0 < kQSteps; i0 += 8) {
-      uint4 x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int row = (i0 + i) * kQRows + lane / kQLanes;
-        const size_t from = __shfl_sync(0xffffffffu, my_row, row);
-        x[i] = make_uint4(0, 0, 0, 0);
-        if ((R & ~31) + row < live)
-          x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + from * D) + lane % kQLanes);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
+        const uint4 x = q_raw[i];
+        if constexpr (kQSteps > 8) q_raw[i] = q_raw[i + 8];
         const int row = (r & ~31) + (i0 + i) * kQRows + lane / kQLanes, c = lane % kQLanes;  // of the tile
         const uint32_t kAbs = 0x7fff7fffu;
-        uint32_t am = __vmaxu2(__vmaxu2(x[i].x & kAbs, x[i].y & kAbs), __vmaxu2(x[i].z & kAbs, x[i].w & kAbs));
+        uint32_t am = __vmaxu2(__vmaxu2(x.x & kAbs, x.y & kAbs), __vmaxu2(x.z & kAbs, x.w & kAbs));
 #pragma unroll
         for (int o = 1; o < kQLanes; o <<= 1) am = __vmaxu2(am, __shfl_xor_sync(0xffffffffu, am, o));
         const int eq = exponent_below(__uint_as_float(max(am & 0xffffu, am >> 16) << 16), 15);
@@ -531,9 +534,9 @@ __global__ void __launch_bounds__(512, 1)
         const float sc_i = __shfl_sync(0xffffffffu, fmaxf(p.scale_log2 * exp2i(-eq), 0x1p-126f),
                                        lane % kQRows * kQLanes);
         if (lane / kQRows == i0 + i) sc = sc_i;
-        if (kStream && (i & 1) != t) continue;
+        if (kStream && (i & 1) != t) continue;  // each warpgroup lays out half of the rows
         const float qs = exp2i(eq);
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
         float f[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
