@@ -139,37 +139,44 @@ class Case:
             scale=self.scale, **kw)
 
     def keys(self, w, b):
-        j, P = np.arange(self.prefix), self.P
-        pg, r = self.pt[j // P], j % P
+        """[Hkv, n, D]: the prefix's rows, then the sequence's own."""
+        if not hasattr(self, "_prefix"):
+            self._prefix = {}
+        if (w, self.prefix) not in self._prefix:
+            j = np.arange(self.prefix)
+            self._prefix[w, self.prefix] = self._rows(w, self.pt[j // self.P], j % self.P)
         i = np.arange(self.lens[b])
-        pg, r = np.concatenate([pg, self.bt[b, i // P]]), np.concatenate([r, i % P])
-        return self.codes[w][pg, r] * self.scales[w][pg, r].astype(np.float64)[..., None]  # [n, Hkv, D]
+        own = self._rows(w, self.bt[b, i // self.P], i % self.P)
+        return np.concatenate([self._prefix[w, self.prefix], own], 1)
+
+    def _rows(self, w, pg, r):
+        return (self.codes[w][pg, r] * self.scales[w][pg, r].astype(np.float64)[..., None]).transpose(1, 0, 2)
 
     def check(self, o, lse):
         o, lse = bf16_to_f64(_bits(o)), lse.cpu().numpy().astype(np.float64)
-        G = self.Hq // self.Hkv
+        Hkv, G = self.Hkv, self.Hq // self.Hkv
         q = bf16_to_f64(self.qb)
         for b in range(self.B):
             k, v = self.keys(0, b), self.keys(1, b)
-            n = len(k)
+            n = k.shape[1]
             if n == 0:
                 assert (o[b] == 0).all() and np.isneginf(lse[b]).all()
                 continue
-            for h in range(self.Hq):
-                kh, vh, qh = k[:, h // G], v[:, h // G], q[b, 0, h]
-                x = self.scale * (kh @ qh)
-                X = self.scale * (np.abs(kh) @ np.abs(qh)).max()
-                top = x.max()
-                p = np.exp(x - top)
-                total = p.sum()
-                want, size = p @ vh / total, p @ np.abs(vh) / total
-                L = top + np.log(total)
-                weight = 2 * 2.0 ** -15 * X + 2.0 ** -20
-                tol = (2.0 ** -8 * np.abs(want) + (3 * 2.0 ** -11 + weight) * size +
-                       (n + 1) * 2.0 ** -30 * np.abs(vh).max() + 1e-38)
-                bad = ~(np.abs(o[b, 0, h] - want) <= tol)
-                assert not bad.any(), (b, h, np.abs(o[b, 0, h] - want).max(), tol.min())
-                assert abs(lse[b, h] - L) <= 2.0 ** -15 * X + 2.0 ** -20 + 2.0 ** -21 * abs(L), (b, h, lse[b, h], L)
+            qb = q[b, 0].reshape(Hkv, G, self.D)
+            x = self.scale * (qb @ k.transpose(0, 2, 1))  # [Hkv, G, n]
+            X = self.scale * (np.abs(qb) @ np.abs(k).transpose(0, 2, 1)).max(-1)
+            top = x.max(-1, keepdims=True)
+            p = np.exp(x - top)
+            total = p.sum(-1)
+            want, size = p @ v / total[..., None], p @ np.abs(v) / total[..., None]
+            L = top[..., 0] + np.log(total)
+            weight = (2 * 2.0 ** -15 * X + 2.0 ** -20)[..., None]
+            tol = (2.0 ** -8 * np.abs(want) + (3 * 2.0 ** -11 + weight) * size +
+                   (n + 1) * 2.0 ** -30 * np.abs(v).max((1, 2))[:, None, None] + 1e-38)
+            err = np.abs(o[b, 0].reshape(Hkv, G, self.D) - want)
+            assert (err <= tol).all(), (b, np.argwhere(~(err <= tol))[0], err.max())
+            err = np.abs(lse[b].reshape(Hkv, G) - L)
+            assert (err <= 2.0 ** -15 * X + 2.0 ** -20 + 2.0 ** -21 * np.abs(L)).all(), (b, err.max())
 
 
 CASES = [  # bits, B, Hq, Hkv, D, P, prefix, own lengths, num_splits
@@ -204,6 +211,51 @@ def test_matches_definition(built, bits, B, Hq, Hkv, D, P, prefix, lens, splits)
     assert fa.fa_device_status() == 0
 
 
+# The same where the rows and the tiles per SM are many enough for the tcgen05 kernel: 128 rows a CTA as two
+# streams of tiles (1, 2 and 3 tiles), blocks of 256 rows (whole, part, several), padding rows, every page size.
+WIDE = [
+    (8, 16, 736, 92, 64, 64, 1, [b % 3 for b in range(16)], 0),         # R = 128, one key
+    (4, 16, 736, 92, 128, 16, 127, list(range(16)), 0),                 # one tile
+    (8, 32, 384, 96, 128, 64, 129, [5 * b for b in range(32)], 1),      # two tiles, the second of one key
+    (8, 13, 280, 40, 64, 32, 1000, [300 - 20 * b for b in range(13)], 0),  # R = 91, splits of 2 and 3 tiles
+    (4, 13, 28, 4, 128, 16, 9003, [60 * b for b in range(13)], 3),
+    (8, 13, 16, 2, 128, 256, 9500, [300 - 20 * b for b in range(13)], 0),
+    (8, 43, 150, 50, 128, 64, 200, [3] * 43, 0),                        # R = 129
+    (4, 16, 480, 30, 128, 16, 515, [9 * b for b in range(16)], 0),      # R = 256
+    (8, 12, 232, 1, 64, 64, 641, [40, 0, 129] * 4, 0),                  # R = 2784: 11 blocks
+    (4, 5, 116, 1, 64, 64, 3500, [1, 2, 3, 4, 5], 2),                   # R = 580
+    (8, 10, 64, 2, 128, 128, 3001, [100] * 10, 4),                      # R = 320: a block of 64 rows
+]
+
+
+@gpu
+@pytest.mark.parametrize("bits,B,Hq,Hkv,D,P,prefix,lens,splits", WIDE)
+def test_wide_matches_definition(built, bits, B, Hq, Hkv, D, P, prefix, lens, splits):
+    c = Case(bits, B, Hq, Hkv, D, P, prefix, lens)
+    c.check(*c.call(splits))
+    assert fa.fa_device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("prefix", [0, 1, 130])
+def test_prefix_shorter_than_its_table(built, prefix):
+    """The launch follows the table's size, the work the length on the device."""
+    c = Case(8, 16, 480, 30, 128, 16, 700, [0, 1, 30, 200] * 4)
+    c.prefix = prefix
+    c.dev["pl"].fill_(prefix)
+    c.check(*c.call())
+    assert fa.fa_device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("kind", ["scales", "peaked", "rows"])
+@pytest.mark.parametrize("B,Hq,Hkv,D,prefix", [(16, 192, 24, 128, 700), (20, 192, 24, 64, 700)])
+def test_wide_ranges(built, bits, kind, B, Hq, Hkv, D, prefix):
+    c = Case(bits, B, Hq, Hkv, D, 64, prefix, [(37 * b) % 100 for b in range(B)], kind=kind)
+    c.check(*c.call())
+
+
 @gpu
 @pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("kind", ["scales", "peaked", "rows"])
@@ -236,9 +288,10 @@ def test_equals_paged_decode_over_joined_tables(built):
 
 
 @gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("what", ["prefix page", "negative page", "prefix_len", "negative prefix_len", "page", "len"])
-def test_bad_indices_are_reported(built, what):
-    c = Case(8, 3, 8, 2, 64, 16, 200, [20, 30, 0])
+def test_bad_indices_are_reported(built, what, wide):
+    c = Case(8, 43, 240, 80, 64, 16, 200, [20, 30, 0] + [1] * 40) if wide else Case(8, 3, 8, 2, 64, 16, 200, [20, 30, 0])
     d = c.dev
     if what == "prefix page":
         d["pt"][3] = c.pool[0].shape[0]
@@ -259,12 +312,12 @@ def test_bad_indices_are_reported(built, what):
 
 
 @gpu
-@pytest.mark.parametrize("B", [2, 40])
-def test_nan_rows(built, B):
+@pytest.mark.parametrize("B,Hkv", [(2, 2), (40, 2), (32, 64), (40, 64)])  # (64: the tcgen05 kernel)
+def test_nan_rows(built, B, Hkv):
     """A row written from NaN (scale NaN): who reads it is NaN, the others are as they were; NaN in rows that
     nobody reads (the rest of the last pages) changes nothing."""
     import torch
-    c = Case(8, B, 8, 2, 64, 64, 200, [30 + b for b in range(B)])
+    c = Case(8, B, 4 * Hkv, Hkv, 64, 64, 200, [30 + b for b in range(B)])
     d = c.dev
     for s in (d["ks"], d["vs"]):
         s[int(c.pt[3]), :, 200 % 64:] = float("nan")
@@ -277,8 +330,9 @@ def test_nan_rows(built, B):
         pg = int(c.pt[1])
         s[pg, 1, 7] = float("nan")
         o, lse = c.call()
-        assert torch.isnan(o[:, 0, 4:]).all() and not torch.isnan(o[:, 0, :4]).any()
-        assert torch.isnan(lse[:, 4:]).all() == (which == "ks") and not torch.isnan(lse[:, :4]).any()
+        assert torch.isnan(o[:, 0, 4:8]).all() and torch.isnan(lse[:, 4:8]).all() == (which == "ks")
+        o[:, 0, 4:8], lse[:, 4:8] = 0, 0
+        assert not torch.isnan(o).any() and not torch.isnan(lse).any()
         s[pg, 1, 7] = 1.0
         own = int(c.bt[1, 0])
         s[own, 0, 3] = float("nan")
@@ -290,10 +344,11 @@ def test_nan_rows(built, B):
 
 
 @gpu
-def test_offsets_past_32_bits(built):
+@pytest.mark.parametrize("B,G,prefix", [(4, 1, 150), (16, 8, 1500)])
+def test_offsets_past_32_bits(built, B, G, prefix):
     """A prefix in the last pages of a pool of more than 2^32 bytes of codes."""
     import torch
-    c = Case(8, 4, 8, 8, 128, 64, 150, [3, 70, 1, 0])
+    c = Case(8, B, 8 * G, 8, 128, 64, prefix, [3, 70, 1, 0] * (B // 4))
     d, n = c.dev, c.pool[0].shape[0]
     pages = 2 ** 32 // (64 * 8 * 128) + n
     for key in ("kp", "vp", "ks", "vs"):
@@ -307,18 +362,20 @@ def test_offsets_past_32_bits(built):
 
 
 @gpu
-def test_step_captured_and_replayed(built):
+@pytest.mark.parametrize("Hkv,G", [(2, 4), (46, 33)])  # (33 x 4 rows: the tcgen05 kernel)
+def test_step_captured_and_replayed(built, Hkv, G):
     """A serving step (append the step's token, then decode) captured once and replayed while lengths, prefix and
     inputs change in place; a second graph with its own workspace; outputs of a replay do not change between runs."""
     import torch
     lens = [40, 63, 64, 10]
-    c = Case(8, 4, 8, 2, 128, 64, 333, [n + 3 for n in lens], spare=4)
+    Hq = Hkv * G
+    c = Case(8, 4, Hq, Hkv, 128, 64, 333, [n + 3 for n in lens], spare=4)
     d = c.dev
     d["sl"].copy_(torch.tensor(lens, dtype=torch.int32))
-    o, lse = torch.empty_like(d["q"]), torch.empty(4, 8, device="cuda")
-    ws = torch.empty(fa.fa_decode_shared_workspace_bytes(4, 8, 2, 128, len(c.pt) * 64, c.bt.shape[1] * 64),
+    o, lse = torch.empty_like(d["q"]), torch.empty(4, Hq, device="cuda")
+    ws = torch.empty(fa.fa_decode_shared_workspace_bytes(4, Hq, Hkv, 128, len(c.pt) * 64, c.bt.shape[1] * 64),
                      dtype=torch.uint8, device="cuda")
-    k, v = (torch.empty(4, 1, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, v = (torch.empty(4, 1, Hkv, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
     k.zero_()
     v.zero_()
 
@@ -338,7 +395,7 @@ def test_step_captured_and_replayed(built):
     with torch.cuda.graph(g):
         step()
     for i in range(3):
-        kb, vb = (make_rows(70 + 2 * i + w, (4, 1, 2, 128), "normal") for w in range(2))
+        kb, vb = (make_rows(70 + 2 * i + w, (4, 1, Hkv, 128), "normal") for w in range(2))
         k.copy_(_bf16(kb))
         v.copy_(_bf16(vb))
         if i == 2:
@@ -362,7 +419,7 @@ def test_step_captured_and_replayed(built):
 def test_two_streams_at_once(built):
     import torch
     c = Case(8, 8, 32, 8, 128, 64, 3000, [100] * 8)
-    e = Case(4, 20, 28, 4, 128, 16, 2000, [64] * 20, seed=7)
+    e = Case(4, 20, 28, 4, 128, 16, 5000, [64] * 20, seed=7)
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
     outs = []

@@ -180,16 +180,18 @@ __device__ __forceinline__ void cp_async_wait_all() {
 }
 
 // Shape constants of the decode kernels.
-constexpr int kDecodeStages = 2;      // K/V stages of 128 keys in the shared-memory ring (3 CTAs per SM)
+// K/V stages of 128 keys in the shared-memory ring: 2 in each of 3 CTAs per SM; CTAs of two blocks of heads
+// (2 per SM, for their registers) have 3
+constexpr int kDecodeStages = 2;
 constexpr int kDecodeMinChunk = 128;  // smallest split, in keys; a multiple of 128
 
 // Shared-memory plan of the split kernel.  A stage holds 128 keys: the K and V code tiles
 // ([128 rows][kRow bytes], swizzled like the TMA box so that the row-per-lane fragment reads
 // spread over the banks) and their fp32 scales.
-template <int D, int kBits>
+template <int D, int kBits, int kHB = 1>
 struct DecodeCfg {
   static constexpr int kT = 128;                  // keys per stage
-  static constexpr int kStages = kDecodeStages;
+  static constexpr int kStages = kHB == 1 ? kDecodeStages : 3;
   static constexpr int kRow = D * kBits / 8;      // bytes of one key row of codes
   static constexpr int kTile = kT * kRow;         // bytes of one K or V code tile
   static constexpr int kStageBytes = 2 * kTile;
@@ -236,13 +238,12 @@ __device__ __forceinline__ uint32_t nib_hi16_f16x2(uint32_t raw) {
   return d;
 }
 
-// 3 CTAs per SM for the 8-bit kernels (at most 136 registers a thread): the bytes in flight
-// per SM set the decode's bandwidth.
-template <int D, bool kPaged, int kBits>
-__global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kernel(
-    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-    const DecodeParams p) {
-  using C = DecodeCfg<D, kBits>;
+// The split kernel for kHB blocks of 8 query heads per CTA: with two, both use each converted K and V
+// fragment, which is most of the work.
+template <int D, bool kPaged, int kBits, int kHB>
+__device__ __forceinline__ void decode_split(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                             const DecodeParams& p) {
+  using C = DecodeCfg<D, kBits, kHB>;
   constexpr int KS = D / 16;            // QK k-steps
   constexpr int MT = D / 16;            // PV m-tiles (16 output dims each)
   constexpr int QD = D / 4;             // QK: dims of each key row held by one thread
@@ -269,9 +270,9 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
   // grid (Hkv, splits, B * head blocks): the KV head varies fastest, so CTAs running at the
   // same time stream the same key rows (all KV heads of a key are contiguous in memory).
   const int kvh = blockIdx.x, split = blockIdx.y;
-  const int nhb = (p.G + 7) / 8;
+  const int nhb = (p.G + 8 * kHB - 1) / (8 * kHB);
   int b = static_cast<int>(blockIdx.z) / nhb;
-  const int hb = static_cast<int>(blockIdx.z) % nhb;
+  const int hb = static_cast<int>(blockIdx.z) % nhb * kHB;
   if constexpr (kPaged) {
     // Longest sequences first: with mixed lengths a split's work is proportional to its
     // sequence's length, and CTAs start in grid order, so the long ones go in the first wave
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
     else
       return static_cast<size_t>(b) * p.Hq + head0 + i;
   };
-  const int nheads = min(8, p.G - hb * 8);
+  const int nheads = min(8 * kHB, p.G - hb * 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   int len = p.Skv;
@@ -470,12 +471,14 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
   // Thread c holds dims [QD*c, QD*c + QD) of its head, in the order its K fragment takes them
   // from each key row: INT8 k-step s, element e is dim 4s + e of the block; INT4 k-step 2j + h
   // takes nibbles (2h, 2h+4) and (2h+1, 2h+5) of word j, i.e. dims 8j + 2h + {0, 4, 1, 5}.
-  uint32_t qf[KS][2];
-  float sc_mine;
-  {
+  uint32_t qf[kHB][KS][2];
+  float sc0[kHB], sc1[kHB];  // of this thread's accumulator columns, heads 2c and 2c + 1 of a block
+#pragma unroll
+  for (int z = 0; z < kHB; ++z) {
+    float sc_mine;
     float qv[KS][4];
-    const bool hv = g < nheads;
-    const uint16_t* qrow = p.q + row_of(hv ? g : 0) * D;
+    const bool hv = 8 * z + g < nheads;
+    const uint16_t* qrow = p.q + row_of(hv ? 8 * z + g : 0) * D;
     float amax = 0.f;
     uint4 raw[QD / 8];
 #pragma unroll
@@ -500,19 +503,24 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
     const float qs_hi = kBits == 4 ? qs * 0.0625f : qs;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      qf[s][0] = pack_f16x2(qv[s][0] * qs, qv[s][1] * qs);
-      qf[s][1] = pack_f16x2(qv[s][2] * qs_hi, qv[s][3] * qs_hi);
+      qf[z][s][0] = pack_f16x2(qv[s][0] * qs, qv[s][1] * qs);
+      qf[z][s][1] = pack_f16x2(qv[s][2] * qs_hi, qv[s][3] * qs_hi);
     }
     sc_mine = p.scale_log2 * exp2i(-eq);
+    sc0[z] = __shfl_sync(0xffffffffu, sc_mine, 8 * c);
+    sc1[z] = __shfl_sync(0xffffffffu, sc_mine, 8 * c + 4);
   }
-  // this thread's accumulator columns are heads 2c and 2c+1
-  const float sc0 = __shfl_sync(0xffffffffu, sc_mine, 8 * c);
-  const float sc1 = __shfl_sync(0xffffffffu, sc_mine, 8 * c + 4);
 
-  float oacc[MT][4];
+  float oacc[kHB][MT][4];
+  float m0[kHB], m1[kHB], l0[kHB], l1[kHB];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) oacc[mt][0] = oacc[mt][1] = oacc[mt][2] = oacc[mt][3] = 0.f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  for (int z = 0; z < kHB; ++z) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+      oacc[z][mt][0] = oacc[z][mt][1] = oacc[z][mt][2] = oacc[z][mt][3] = 0.f;
+    m0[z] = m1[z] = -INFINITY;
+    l0[z] = l1[z] = 0.f;
+  }
   // P' = p * v_scale * 2^E must stay below 2^15 in fp16 (p <= 2^8 with the lazy rescale): the
   // warp lowers E, rescaling its output accumulator, whenever a larger v_scale arrives.
   constexpr int kEUnset = 1 << 20;
@@ -528,7 +536,7 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
       const int r_w = 32 * warp;  // first row of this warp in the stage tiles
 
       // -- S = Kcode . Q^T per 16-key group; x = score in log2 units --
-      float x[2][4];
+      float x[kHB][2][4];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint32_t kw[2][QW];  // this thread's words of rows g and g + 8 of the group
@@ -550,61 +558,77 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
             }
           }
         }
-        float sacc[4] = {0.f, 0.f, 0.f, 0.f};
+        float sacc[kHB][4];
+#pragma unroll
+        for (int z = 0; z < kHB; ++z) sacc[z][0] = sacc[z][1] = sacc[z][2] = sacc[z][3] = 0.f;
 #pragma unroll
         for (int st = 0; st < KS; ++st) {
+          uint32_t a0, a1, a2, a3;
           if constexpr (kBits == 8) {
             const uint32_t w0 = kw[0][st], w1 = kw[1][st];
-            mma_f16_16816(sacc, codes_to_f16x2(w0, kSelB01), codes_to_f16x2(w1, kSelB01),
-                          codes_to_f16x2(w0, kSelB23), codes_to_f16x2(w1, kSelB23), qf[st][0],
-                          qf[st][1]);
+            a0 = codes_to_f16x2(w0, kSelB01);
+            a1 = codes_to_f16x2(w1, kSelB01);
+            a2 = codes_to_f16x2(w0, kSelB23);
+            a3 = codes_to_f16x2(w1, kSelB23);
           } else {
             // k-step 2j + h of word j: nibbles (2h, 2h+4) as is, (2h+1, 2h+5) times 16
             const uint32_t w0 = kw[0][st >> 1] >> (8 * (st & 1));
             const uint32_t w1 = kw[1][st >> 1] >> (8 * (st & 1));
-            mma_f16_16816(sacc, nib_lo_f16x2(w0), nib_lo_f16x2(w1), nib_hi16_f16x2(w0),
-                          nib_hi16_f16x2(w1), qf[st][0], qf[st][1]);
+            a0 = nib_lo_f16x2(w0);
+            a1 = nib_lo_f16x2(w1);
+            a2 = nib_hi16_f16x2(w0);
+            a3 = nib_hi16_f16x2(w1);
           }
+#pragma unroll
+          for (int z = 0; z < kHB; ++z)
+            mma_f16_16816(sacc[z], a0, a1, a2, a3, qf[z][st][0], qf[z][st][1]);
         }
         const int rA = r_w + 16 * u + kslot(g), rB = r_w + 16 * u + kslot(g + 8);
         const int tA = T + 16 * u + kslot(g), tB = T + 16 * u + kslot(g + 8);
         const float kA = lds32f(ks_s + 4 * rA), kB = lds32f(ks_s + 4 * rB);
-        x[u][0] = tA < t_end ? sacc[0] * kA * sc0 : -INFINITY;
-        x[u][1] = tA < t_end ? sacc[1] * kA * sc1 : -INFINITY;
-        x[u][2] = tB < t_end ? sacc[2] * kB * sc0 : -INFINITY;
-        x[u][3] = tB < t_end ? sacc[3] * kB * sc1 : -INFINITY;
+#pragma unroll
+        for (int z = 0; z < kHB; ++z) {
+          x[z][u][0] = tA < t_end ? sacc[z][0] * kA * sc0[z] : -INFINITY;
+          x[z][u][1] = tA < t_end ? sacc[z][1] * kA * sc1[z] : -INFINITY;
+          x[z][u][2] = tB < t_end ? sacc[z][2] * kB * sc0[z] : -INFINITY;
+          x[z][u][3] = tB < t_end ? sacc[z][3] * kB * sc1[z] : -INFINITY;
+        }
       }
 
       // -- online softmax per head (columns 2c, 2c+1); max over the warp's 32 keys --
-      float mx0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-      float mx1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+      float mu0[kHB], mu1[kHB];
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-      }
-      if (mx0 > m0 + 8.f) {
-        const float a = ex2(m0 - mx0);
-        m0 = mx0;
-        l0 *= a;
+      for (int z = 0; z < kHB; ++z) {
+        float mx0 = fmaxf(fmaxf(x[z][0][0], x[z][0][2]), fmaxf(x[z][1][0], x[z][1][2]));
+        float mx1 = fmaxf(fmaxf(x[z][0][1], x[z][0][3]), fmaxf(x[z][1][1], x[z][1][3]));
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          oacc[mt][0] *= a;
-          oacc[mt][2] *= a;
+        for (int o = 4; o < 32; o <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
         }
-      }
-      if (mx1 > m1 + 8.f) {
-        const float a = ex2(m1 - mx1);
-        m1 = mx1;
-        l1 *= a;
+        if (mx0 > m0[z] + 8.f) {
+          const float a = ex2(m0[z] - mx0);
+          m0[z] = mx0;
+          l0[z] *= a;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          oacc[mt][1] *= a;
-          oacc[mt][3] *= a;
+          for (int mt = 0; mt < MT; ++mt) {
+            oacc[z][mt][0] *= a;
+            oacc[z][mt][2] *= a;
+          }
         }
+        if (mx1 > m1[z] + 8.f) {
+          const float a = ex2(m1[z] - mx1);
+          m1[z] = mx1;
+          l1[z] *= a;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            oacc[z][mt][1] *= a;
+            oacc[z][mt][3] *= a;
+          }
+        }
+        mu0[z] = (m0[z] == -INFINITY) ? 0.f : m0[z];
+        mu1[z] = (m1[z] == -INFINITY) ? 0.f : m1[z];
       }
-      const float mu0 = (m0 == -INFINITY) ? 0.f : m0;
-      const float mu1 = (m1 == -INFINITY) ? 0.f : m1;
 
       // -- value scales of the warp's keys; lower E if a larger one arrived --
       float vsc[2][2];
@@ -624,28 +648,32 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
         if (E != kEUnset) {
           const float a = exp2i_or_zero(e_step - E);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            oacc[mt][0] *= a;
-            oacc[mt][1] *= a;
-            oacc[mt][2] *= a;
-            oacc[mt][3] *= a;
-          }
+          for (int z = 0; z < kHB; ++z)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              oacc[z][mt][0] *= a;
+              oacc[z][mt][1] *= a;
+              oacc[z][mt][2] *= a;
+              oacc[z][mt][3] *= a;
+            }
         }
         E = e_step;
       }
       const float pscale = exp2i(E);
 
-      uint32_t pb[2][2];  // PV B operand per group: keys 0-7 and 8-15 of the group
+      uint32_t pb[kHB][2][2];  // PV B operand per group: keys 0-7 and 8-15 of the group
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float pa0 = ex2(x[u][0] - mu0), pa1 = ex2(x[u][1] - mu1);
-        const float pb0 = ex2(x[u][2] - mu0), pb1 = ex2(x[u][3] - mu1);
-        l0 += pa0 + pb0;
-        l1 += pa1 + pb1;
-        const float wa = vsc[u][0] * pscale, wb = vsc[u][1] * pscale;
-        pb[u][0] = movmatrix_trans(pack_f16x2(pa0 * wa, pa1 * wa));
-        pb[u][1] = movmatrix_trans(pack_f16x2(pb0 * wb, pb1 * wb));
-      }
+      for (int z = 0; z < kHB; ++z)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float pa0 = ex2(x[z][u][0] - mu0[z]), pa1 = ex2(x[z][u][1] - mu1[z]);
+          const float pb0 = ex2(x[z][u][2] - mu0[z]), pb1 = ex2(x[z][u][3] - mu1[z]);
+          l0[z] += pa0 + pb0;
+          l1[z] += pa1 + pb1;
+          const float wa = vsc[u][0] * pscale, wb = vsc[u][1] * pscale;
+          pb[z][u][0] = movmatrix_trans(pack_f16x2(pa0 * wa, pa1 * wa));
+          pb[z][u][1] = movmatrix_trans(pack_f16x2(pb0 * wb, pb1 * wb));
+        }
 
       // -- O^T += Vcode^T . P'^T --
 #pragma unroll
@@ -695,7 +723,9 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
             a2 = nib_lo_f16x2(x89);
             a3 = nib_hi16_f16x2(x89);
           }
-          mma_f16_16816(oacc[mt], a0, a1, a2, a3, pb[u][0], pb[u][1]);
+#pragma unroll
+          for (int z = 0; z < kHB; ++z)
+            mma_f16_16816(oacc[z][mt], a0, a1, a2, a3, pb[z][u][0], pb[z][u][1]);
         }
       }
     }
@@ -707,75 +737,97 @@ __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kerne
   // depends on: whoever waits for this one then waits for both.
   if constexpr (kPaged) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // ---- merge the 4 warps (the stage tiles are free now: every stage has been consumed) ----
-  named_bar_sync(1, 128);
+  // ---- merge the 4 warps, 8 heads at a time (the stage tiles are free now: every stage has been
+  // consumed) ----
   float* sm_o = reinterpret_cast<float*>(smem + C::kMergeO);
   float* sm_m = reinterpret_cast<float*>(smem + C::kMergeM);
   float* sm_l = reinterpret_cast<float*>(smem + C::kMergeL);
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, o);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-  }
-  if (g == 0) {
-    sm_m[warp * 8 + 2 * c] = m0;
-    sm_m[warp * 8 + 2 * c + 1] = m1;
-    sm_l[warp * 8 + 2 * c] = l0;
-    sm_l[warp * 8 + 2 * c + 1] = l1;
-  }
   const float unscale = (E == kEUnset) ? 0.f : exp2i_or_zero(-E);
   // INT4: the odd dims (rows g + 8 of each m-tile) were accumulated from 16 x the codes
   const float unscale_hi = kBits == 4 ? unscale * 0.0625f : unscale;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int d0 = DPT * g + 2 * mt;
-    float* ow = sm_o + warp * 8 * D;
-    ow[(2 * c) * D + d0] = oacc[mt][0] * unscale;
-    ow[(2 * c + 1) * D + d0] = oacc[mt][1] * unscale;
-    ow[(2 * c) * D + d0 + 1] = oacc[mt][2] * unscale_hi;
-    ow[(2 * c + 1) * D + d0 + 1] = oacc[mt][3] * unscale_hi;
-  }
-  named_bar_sync(1, 128);
-  for (int idx = threadIdx.x; idx < nheads * (D / 4); idx += 128) {  // 4 dims
-    const int h = idx / (D / 4), d = idx % (D / 4) * 4;
-    float M = -INFINITY;
+  for (int z = 0; z < kHB; ++z) {
+    named_bar_sync(1, 128);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, sm_m[w * 8 + h]);
-    // a sum of 0 means no key; a NaN among the scales (a row written from a NaN) stays one
-    float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float mw = sm_m[w * 8 + h];
-      const float f = (mw == -INFINITY) ? 0.f : ex2(mw - M);
-      L += f * sm_l[w * 8 + h];
-      const float4 o = *reinterpret_cast<const float4*>(sm_o + (w * 8 + h) * D + d);
-      acc.x += f * o.x;
-      acc.y += f * o.y;
-      acc.z += f * o.z;
-      acc.w += f * o.w;
+    for (int o = 4; o < 32; o <<= 1) {
+      l0[z] += __shfl_xor_sync(0xffffffffu, l0[z], o);
+      l1[z] += __shfl_xor_sync(0xffffffffu, l1[z], o);
     }
-    const size_t row = static_cast<size_t>(split) * p.rows + row_of(h);
-    *reinterpret_cast<float4*>(p.o_part + row * D + d) =
-        (L == 0.f) ? make_float4(0.f, 0.f, 0.f, 0.f)
-                   : make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L);
-    if (d == 0) p.lse_part[row] = (L == 0.f) ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+    if (g == 0) {
+      sm_m[warp * 8 + 2 * c] = m0[z];
+      sm_m[warp * 8 + 2 * c + 1] = m1[z];
+      sm_l[warp * 8 + 2 * c] = l0[z];
+      sm_l[warp * 8 + 2 * c + 1] = l1[z];
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int d0 = DPT * g + 2 * mt;
+      float* ow = sm_o + warp * 8 * D;
+      ow[(2 * c) * D + d0] = oacc[z][mt][0] * unscale;
+      ow[(2 * c + 1) * D + d0] = oacc[z][mt][1] * unscale;
+      ow[(2 * c) * D + d0 + 1] = oacc[z][mt][2] * unscale_hi;
+      ow[(2 * c + 1) * D + d0 + 1] = oacc[z][mt][3] * unscale_hi;
+    }
+    named_bar_sync(1, 128);
+    for (int idx = threadIdx.x; idx < min(8, nheads - 8 * z) * (D / 4); idx += 128) {  // 4 dims
+      const int h = idx / (D / 4), d = idx % (D / 4) * 4;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, sm_m[w * 8 + h]);
+      // a sum of 0 means no key; a NaN among the scales (a row written from a NaN) stays one
+      float L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float mw = sm_m[w * 8 + h];
+        const float f = (mw == -INFINITY) ? 0.f : ex2(mw - M);
+        L += f * sm_l[w * 8 + h];
+        const float4 o = *reinterpret_cast<const float4*>(sm_o + (w * 8 + h) * D + d);
+        acc.x += f * o.x;
+        acc.y += f * o.y;
+        acc.z += f * o.z;
+        acc.w += f * o.w;
+      }
+      const size_t row = static_cast<size_t>(split) * p.rows + row_of(8 * z + h);
+      *reinterpret_cast<float4*>(p.o_part + row * D + d) =
+          (L == 0.f) ? make_float4(0.f, 0.f, 0.f, 0.f)
+                     : make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L);
+      if (d == 0) p.lse_part[row] = (L == 0.f) ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+    }
   }
 }
 
-// One warp per (batch, query head): the lanes read the splits' log-sum-exps together, reduce
-// the maximum and the sum of weights with shuffles, then each lane merges D/32 output dims with
-// vector loads, several splits in flight at once.  Launched as a programmatic dependent of the
-// split kernel: its CTAs may start while the split kernel drains and wait at griddepcontrol.wait
-// until every partial is written and visible.
-template <int D>
+// 3 CTAs per SM for the 8-bit kernels (at most 136 registers a thread): the bytes in flight
+// per SM set the decode's bandwidth.
+template <int D, bool kPaged, int kBits>
+__global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const DecodeParams p) {
+  decode_split<D, kPaged, kBits, 1>(tm_k, tm_v, p);
+}
+
+// Two blocks of 8 query heads per CTA, over a paged cache.
+template <int D, int kBits>
+__global__ void __launch_bounds__(160, 2) fa_decode_split16_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const DecodeParams p) {
+  decode_split<D, true, kBits, 2>(tm_k, tm_v, p);
+}
+
+// Merge kernel: kWarps warps per (batch, query head), 4 warps a block.  A warp takes every kWarps-th
+// split: the lanes read the splits' log-sum-exps together and reduce the maximum with shuffles, then each
+// lane merges D/32 output dims with vector loads, several splits in flight at once.  Launched as a
+// programmatic dependent of the split kernel: its CTAs may start while the split kernel drains and
+// wait at griddepcontrol.wait until every partial is written and visible.
+template <int D, int kWarps = 1>
 __global__ void __launch_bounds__(128) fa_decode_combine_kernel(const CombineParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int V = D / 32;  // dims per lane
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x * (4 / kWarps) + warp / kWarps;
   const int rows = p.B * p.Hq;
-  if (row >= rows) return;
+  if (kWarps < 4 && row >= rows) return;
+  const int w0 = warp % kWarps;
   const size_t stride = static_cast<size_t>(rows);
   float M = -INFINITY;
   for (int s = lane; s < p.splits; s += 32) M = fmaxf(M, p.lse_part[s * stride + row]);
@@ -785,18 +837,19 @@ __global__ void __launch_bounds__(128) fa_decode_combine_kernel(const CombinePar
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  // lane i weighs split s0 + i; a split with log-sum-exp -inf holds no key and is not read
-  for (int s0 = 0; s0 < p.splits; s0 += 32) {
-    const float ls = s0 + lane < p.splits ? p.lse_part[(s0 + lane) * stride + row] : -INFINITY;
+  // lane i weighs split s0 + kWarps i; a split with log-sum-exp -inf holds no key and is not read
+  for (int s0 = w0; s0 < p.splits; s0 += 32 * kWarps) {
+    const int own = s0 + kWarps * lane;
+    const float ls = own < p.splits ? p.lse_part[own * stride + row] : -INFINITY;
     const float mine = (ls == -INFINITY) ? 0.f : expf(ls - M);
     L += mine;
     const uint32_t some = __ballot_sync(0xffffffffu, ls != -INFINITY);
-    const int n = min(32, p.splits - s0);
+    const int n = min(32, (p.splits - s0 + kWarps - 1) / kWarps);
 #pragma unroll 8
     for (int s = 0; s < n; ++s) {
       const float w = __shfl_sync(0xffffffffu, mine, s);
       const bool read = some >> s & 1;
-      const float* src = p.o_part + ((s0 + s) * stride + row) * D + V * lane;
+      const float* src = p.o_part + ((s0 + kWarps * s) * stride + row) * D + V * lane;
       if constexpr (V == 4) {
         const float4 x = read ? *reinterpret_cast<const float4*>(src) : make_float4(0, 0, 0, 0);
         acc[0] += w * x.x;
@@ -812,6 +865,21 @@ __global__ void __launch_bounds__(128) fa_decode_combine_kernel(const CombinePar
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if constexpr (kWarps > 1) {
+    static_assert(kWarps == 4, "a block per row");
+    __shared__ float sm_acc[kWarps][D], sm_l[kWarps];
+#pragma unroll
+    for (int i = 0; i < V; ++i) sm_acc[warp][V * lane + i] = acc[i];
+    if (lane == 0) sm_l[warp] = L;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      L += sm_l[w];
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += sm_acc[w][V * lane + i];
+    }
+  }
   const float inv = (L == 0.f) ? 0.f : 1.f / L;
   uint16_t* dst = p.o + static_cast<size_t>(row) * D + V * lane;
   if constexpr (V == 4) {

@@ -357,8 +357,31 @@ int launch_split(const CodeMaps& maps, const fa::DecodeParams& p, bool dependent
                 dependent, stream, maps.k, maps.v, p);
 }
 
+// The same over a paged cache with two blocks of 8 heads per CTA.
+std::atomic<uint64_t> g_attr_decode16[4];
+template <int D, int kBits>
+int launch_split16(const CodeMaps& maps, const fa::DecodeParams& p, bool dependent,
+                   cudaStream_t stream) {
+  using C = fa::DecodeCfg<D, kBits, 2>;
+  const long long gz = static_cast<long long>(p.B) * ((p.G + 15) / 16);
+  if (p.splits > 65535 || gz > 65535) return FA_ERR_INVALID_ARG;
+  auto kernel = fa::fa_decode_split16_kernel<D, kBits>;
+  const int rc = ensure_smem_attr(kernel, C::kSmemBytes,
+                                  g_attr_decode16[(D == 128 ? 2 : 0) + (kBits == 4 ? 1 : 0)]);
+  if (rc != FA_OK) return rc;
+  return launch(kernel, dim3(p.Hkv, p.splits, static_cast<unsigned>(gz)), 160, C::kSmemBytes,
+                dependent, stream, maps.k, maps.v, p);
+}
+// ... as fits the number of query rows per KV head.
+template <int D, int kBits>
+int launch_split_rows(const CodeMaps& maps, const fa::DecodeParams& p, bool dependent,
+                      cudaStream_t stream) {
+  return p.G > 8 ? launch_split16<D, kBits>(maps, p, dependent, stream)
+                 : launch_split<D, true, kBits>(maps, p, dependent, stream);
+}
+
 // Merge of `splits` partials: a programmatic dependent that waits on the device for them.
-template <int D>
+template <int D, int kWarps>
 int launch_combine(const fa::DecodeParams& p, int splits, void* o, float* lse, cudaStream_t stream) {
   fa::CombineParams cp{};
   cp.o_part = p.o_part;
@@ -368,8 +391,9 @@ int launch_combine(const fa::DecodeParams& p, int splits, void* o, float* lse, c
   cp.B = p.B;
   cp.Hq = p.Hq;
   cp.splits = splits;
-  const unsigned blocks = static_cast<unsigned>((static_cast<long long>(p.B) * p.Hq + 3) / 4);
-  return launch(fa::fa_decode_combine_kernel<D>, dim3(blocks), 128, 0, true, stream, cp);
+  const long long rows = static_cast<long long>(p.B) * p.Hq;
+  return launch(fa::fa_decode_combine_kernel<D, kWarps>,
+                dim3(static_cast<unsigned>((rows * kWarps + 3) / 4)), 128, 0, true, stream, cp);
 }
 
 // The split kernel, then the merge kernel.  `keys` is the extent of the key axis of the code tensors
@@ -381,7 +405,7 @@ int launch_split_and_combine(const fa::DecodeParams& p, int keys, int outer, voi
   int rc = encode_codes(&maps, p.k, p.v, D * kBits / 8, p.Hkv, keys, outer, kPaged);
   if (rc != FA_OK) return rc;
   if ((rc = launch_split<D, kPaged, kBits>(maps, p, false, stream)) != FA_OK) return rc;
-  return launch_combine<D>(p, p.splits, o, lse, stream);
+  return launch_combine<D, 1>(p, p.splits, o, lse, stream);
 }
 
 template <int D, int kBits>
@@ -519,22 +543,31 @@ int decode_paged(int bits, const void* q, const void* k, const void* v, const fl
 
 constexpr int kSms = 148;
 
-// Up to this many query rows per KV head, the prefix goes through the split kernel as well (8 rows a
-// CTA, its blocks of rows re-reading the tile from L2); above, the tcgen05 kernel's tile of
-// 128 rows pays.
-constexpr int kSharedFewRows = 16;
+// Blocks of heads (or rows) that launch_split_rows makes of G, and its CTAs that fit the GPU at once.
+long long split_blocks(long long G) { return G > 8 ? (G + 15) / 16 : 1; }
+long long split_slots(long long G) { return (G > 8 ? 2 : 3) * kSms; }
 
-// Splits of the prefix.  Few rows: three CTAs of the split kernel per SM.  Otherwise one CTA per SM
-// runs a split of one (KV head, row block) in about (tiles + 3) tile times (start-up, epilogue and
+// Whether the prefix, as one sequence of R rows per KV head, goes through the split kernel too (rows in
+// blocks of 16, each block reading the cache again from L2) or through the tcgen05 kernel (128 or 256
+// rows a tile).  With T tiles of 128 keys per SM, B200, 8 KV heads of 128 dims, INT8:
+//   split 10 us + 1.0 T per block of 16 rows;  tcgen05 14 us + 1.45 T, twice that for a block of 256 rows
+// (131072 keys, T = 55: 16 rows 70 / 93 us, 32 rows 117 / 95 us; 4096 keys, 48 rows 23 / 25 us, 96 rows
+// 29 / 27 us).  At D = 64 a block of 16 costs half, a tcgen05 tile, bound by its softmax, the same.
+bool shared_through_split(int D, long long R, int Hkv, long long max_keys) {
+  const double T = static_cast<double>(Hkv) * ((max_keys + 127) / 128) / kSms;
+  const double tile = R <= 128 ? 1.0 : 2.0 * ((R + 255) / 256);
+  return split_blocks(R) * T < (D == 128 ? 1.45 : 2.2) * tile * T + 4.0;
+}
+
+// Splits of the prefix.  Through the split kernel: what fills the GPU with its CTAs.  Otherwise one CTA per
+// SM runs a split of one (KV head, row block) in about (tiles + 3) tile times (start-up, epilogue and
 // its share of the merge count for three), in as many waves as the CTAs need; the split count with
 // the least total time, the smaller of equals.
-int shared_prefix_splits(int B, int Hq, int Hkv, long long max_keys) {
+int shared_prefix_splits(int D, int B, int Hq, int Hkv, long long max_keys) {
   const long long R = static_cast<long long>(B) * (Hq / Hkv);
   const long long tiles = std::max(1ll, (max_keys + 127) / 128);
-  if (R <= kSharedFewRows) {
-    const long long ctas = Hkv * ((R + 7) / 8);
-    return static_cast<int>(std::min(tiles, std::max(1ll, 3 * kSms / ctas)));
-  }
+  if (shared_through_split(D, R, Hkv, max_keys))
+    return static_cast<int>(std::min(tiles, std::max(1ll, split_slots(R) / (Hkv * split_blocks(R)))));
   const long long base = static_cast<long long>(Hkv) * (R <= 128 ? 1 : (R + 255) / 256);
   int best = 1;
   long long best_cost = -1;
@@ -549,14 +582,15 @@ int shared_prefix_splits(int B, int Hq, int Hkv, long long max_keys) {
 }
 
 // Splits of the sequences' own keys where the caller leaves the choice to the library: pieces of 1024
-// keys (INT4, whose stages take twice as long: 512), as long as three CTAs per SM hold them.  The prefix's
+// keys (INT4, whose stages take twice as long: 512), as long as all CTAs fit the GPU at once.  The prefix's
 // kernel runs beside or right behind this one on the same SMs, so fewer, longer CTAs beat a full
 // GPU: B200, 12 sequences x 232 heads of 64 dims, 256 own keys, 1 / 2 / 4 splits 33 / 39 / 43 us,
 // 8 x 32 heads, 1024 keys 20.5 / 22.5 / 22.6 us; INT4, 13 x 28 heads, 777 keys 32.8 / 28.6 / 28.7 us.
 int shared_own_splits(int bits, int B, int Hq, int Hkv, long long max_keys) {
-  const long long ctas = static_cast<long long>(B) * Hkv * ((Hq / Hkv + 7) / 8);
+  const long long ctas = static_cast<long long>(B) * Hkv * split_blocks(Hq / Hkv);
   const long long keys = bits == 8 ? 1024 : 512;
-  return static_cast<int>(std::max(1ll, std::min(3 * kSms / ctas, (max_keys + keys - 1) / keys)));
+  return static_cast<int>(
+      std::max(1ll, std::min(split_slots(Hq / Hkv) / ctas, (max_keys + keys - 1) / keys)));
 }
 
 std::atomic<uint64_t> g_attr_shared[8];
@@ -593,8 +627,8 @@ int launch_shared(const fa::DecodeParams& own, const fa::SharedParams& sp, void*
   int rc = encode_codes(&maps, own.k, own.v, D * kBits / 8, own.Hkv, 1 << own.page_shift,
                         own.num_pages, true);
   if (rc != FA_OK) return rc;
-  if ((rc = launch_split<D, true, kBits>(maps, own, false, stream)) != FA_OK) return rc;
-  if (sp.R <= kSharedFewRows) {
+  if ((rc = launch_split_rows<D, kBits>(maps, own, false, stream)) != FA_OK) return rc;
+  if (shared_through_split(D, sp.R, sp.Hkv, static_cast<long long>(sp.max_pages) << sp.page_shift)) {
     fa::DecodeParams pre = own;  // one sequence of R rows
     pre.B = 1;
     pre.G = sp.R;
@@ -604,14 +638,18 @@ int launch_shared(const fa::DecodeParams& own, const fa::SharedParams& sp, void*
     pre.max_pages = sp.max_pages;
     pre.o_part = sp.o_part;
     pre.lse_part = sp.lse_part;
-    rc = launch_split<D, true, kBits>(maps, pre, true, stream);
+    rc = launch_split_rows<D, kBits>(maps, pre, true, stream);
   } else if (sp.R <= 128) {
     rc = launch_shared_prefix<D, kBits, true>(maps, sp, stream);
   } else {
     rc = launch_shared_prefix<D, kBits, false>(maps, sp, stream);
   }
   if (rc != FA_OK) return rc;
-  return launch_combine<D>(own, own.splits + sp.splits, o, lse, stream);
+  // four warps per row where one per row leaves the GPU idle over many partials
+  const int splits = own.splits + sp.splits;
+  return splits > 8 && static_cast<long long>(own.B) * own.Hq <= 64 * kSms
+             ? launch_combine<D, 4>(own, splits, o, lse, stream)
+             : launch_combine<D, 1>(own, splits, o, lse, stream);
 }
 
 int page_shift_of(int page_size) {
@@ -734,7 +772,7 @@ bool shared_splits(int bits, int B, int Hq, int Hkv, int D, long long max_prefix
     return false;
   if (static_cast<long long>(B) * Hq > 0x7fffffffLL) return false;
   *own = num_splits > 0 ? num_splits : shared_own_splits(bits, B, Hq, Hkv, max_own);
-  *prefix = shared_prefix_splits(B, Hq, Hkv, max_prefix);
+  *prefix = shared_prefix_splits(D, B, Hq, Hkv, max_prefix);
   return *own <= 65535;
 }
 
