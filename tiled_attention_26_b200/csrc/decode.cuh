@@ -65,6 +65,7 @@ struct DecodeParams {
   const int32_t* block_table;  // [B, max_pages]
   const int32_t* seqlens;      // [B]
   int max_pages, num_pages, page_shift;  // P = 1 << page_shift
+  int min_chunk;  // smallest split, in keys; a multiple of 128
   // Query rows: row i of KV head kvh of sequence b is head kvh * Gq + i % Gq of sequence b + i / Gq
   // of the tensors (G = Gq, i < G: the sequence's own heads).  A prefix that B sequences share is one
   // sequence here, of G = B * Gq rows.
@@ -323,8 +324,8 @@ __device__ __forceinline__ void decode_split(const CUtensorMap& tm_k, const CUte
     }
   }
   // splits are whole stages (every stage starts on a multiple of 128 keys) of at least
-  // kDecodeMinChunk keys: a short sequence takes few splits rather than many tiny ones
-  const int chunk = max(kDecodeMinChunk,
+  // min_chunk keys: a short sequence takes few splits rather than many tiny ones
+  const int chunk = max(kPaged ? p.min_chunk : kDecodeMinChunk,
                         ((len + p.splits - 1) / p.splits + C::kT - 1) / C::kT * C::kT);
   const int t_begin = min(len, split * chunk);
   const int t_end = min(len, t_begin + chunk);

@@ -304,6 +304,7 @@ fa::DecodeParams decode_params(const void* q, const int8_t* k, const int8_t* v, 
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.Gq = p.G;
   p.rows = static_cast<long long>(B) * Hq;
+  p.min_chunk = fa::kDecodeMinChunk;
   return p;
 }
 
@@ -581,16 +582,18 @@ int shared_prefix_splits(int D, int B, int Hq, int Hkv, long long max_keys) {
   return best;
 }
 
-// Splits of the sequences' own keys where the caller leaves the choice to the library: pieces of 1024
-// keys (INT4, whose stages take twice as long: 512), as long as all CTAs fit the GPU at once.  The prefix's
-// kernel runs beside or right behind this one on the same SMs, so fewer, longer CTAs beat a full
-// GPU: B200, 12 sequences x 232 heads of 64 dims, 256 own keys, 1 / 2 / 4 splits 33 / 39 / 43 us,
-// 8 x 32 heads, 1024 keys 20.5 / 22.5 / 22.6 us; INT4, 13 x 28 heads, 777 keys 32.8 / 28.6 / 28.7 us.
-int shared_own_splits(int bits, int B, int Hq, int Hkv, long long max_keys) {
+// Splits of the sequences' own keys where the caller leaves the choice to the library: pieces of 512 keys
+// or more (a sequence no longer than that is one piece), as long as all CTAs fit the GPU at once, or
+// twice as many, of which about half find nothing to do.  The prefix's kernel runs beside or right
+// behind this one on the same SMs, so fewer, longer CTAs beat a full GPU: B200, pieces of 256 / 512 / 1024
+// keys, 32 x 32 heads, 1024 own keys 35.0 / 30.9 / 32.9 us; INT4, 13 x 28 heads, 777 keys 24.7 / 22.6 /
+// 22.6 us; as many splits as fill the GPU, 12 x 232 heads of 64 dims, 256 keys 39 us for 33.
+constexpr int kSharedOwnChunk = 512;
+int shared_own_splits(int B, int Hq, int Hkv, long long max_keys) {
   const long long ctas = static_cast<long long>(B) * Hkv * split_blocks(Hq / Hkv);
-  const long long keys = bits == 8 ? 1024 : 512;
-  return static_cast<int>(
-      std::max(1ll, std::min(split_slots(Hq / Hkv) / ctas, (max_keys + keys - 1) / keys)));
+  const long long fit = split_slots(Hq / Hkv) / ctas;
+  return static_cast<int>(std::max(
+      1ll, std::min(fit == 1 ? 2 : fit, (max_keys + kSharedOwnChunk - 1) / kSharedOwnChunk)));
 }
 
 std::atomic<uint64_t> g_attr_shared[8];
@@ -636,6 +639,7 @@ int launch_shared(const fa::DecodeParams& own, const fa::SharedParams& sp, void*
     pre.block_table = sp.table;
     pre.seqlens = sp.len;
     pre.max_pages = sp.max_pages;
+    pre.min_chunk = fa::kDecodeMinChunk;
     pre.o_part = sp.o_part;
     pre.lse_part = sp.lse_part;
     rc = launch_split_rows<D, kBits>(maps, pre, true, stream);
@@ -765,13 +769,13 @@ int kv_paged(const void* k, const void* v, int64_t k_stride, int64_t v_stride, c
 }
 
 // Sizes of a shared decode call that the workspace depends on; false if they are not valid.
-bool shared_splits(int bits, int B, int Hq, int Hkv, int D, long long max_prefix, long long max_own,
+bool shared_splits(int B, int Hq, int Hkv, int D, long long max_prefix, long long max_own,
                    int num_splits, int* own, int* prefix) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0 || max_prefix <= 0 || max_own <= 0 ||
       num_splits < 0)
     return false;
   if (static_cast<long long>(B) * Hq > 0x7fffffffLL) return false;
-  *own = num_splits > 0 ? num_splits : shared_own_splits(bits, B, Hq, Hkv, max_own);
+  *own = num_splits > 0 ? num_splits : shared_own_splits(B, Hq, Hkv, max_own);
   *prefix = shared_prefix_splits(D, B, Hq, Hkv, max_prefix);
   return *own <= 65535;
 }
@@ -792,7 +796,7 @@ int decode_shared(int bits, const void* q, const void* k, const void* v, const f
   const long long max_own = static_cast<long long>(max_pages) << shift;
   if (max_prefix > (1ll << 30) || max_own > (1ll << 30)) return FA_ERR_INVALID_ARG;
   int own = 0, prefix = 0;
-  if (!shared_splits(bits, B, Hq, Hkv, D, max_prefix, max_own, num_splits, &own, &prefix))
+  if (!shared_splits(B, Hq, Hkv, D, max_prefix, max_own, num_splits, &own, &prefix))
     return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * ((Hq / Hkv + 7) / 8) > 65535) return FA_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
@@ -813,6 +817,7 @@ int decode_shared(int bits, const void* q, const void* k, const void* v, const f
   dp.max_pages = max_pages;
   dp.num_pages = num_pages;
   dp.page_shift = shift;
+  if (num_splits == 0) dp.min_chunk = kSharedOwnChunk;
   fa::SharedParams sp{};
   sp.q = dp.q;
   sp.k_scale = ks;
@@ -1080,8 +1085,7 @@ int fa_kv_gather_int4_paged(const uint8_t* k_pages, const uint8_t* v_pages, cons
 size_t fa_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int D, int max_prefix_len,
                                         int max_seqlen, int num_splits) {
   int own = 0, prefix = 0;
-  // (INT4's splits: never fewer than INT8's)
-  if (!shared_splits(4, B, Hq, Hkv, D, max_prefix_len, max_seqlen, num_splits, &own, &prefix)) return 0;
+  if (!shared_splits(B, Hq, Hkv, D, max_prefix_len, max_seqlen, num_splits, &own, &prefix)) return 0;
   return decode_ws_layout(B, Hq, D, own + prefix, nullptr);
 }
 
