@@ -87,6 +87,20 @@ __device__ __forceinline__ void kv_locate(const KvMap& m, int i, int& page, int&
   }
 }
 
+// Row of the code tensor, and element of the scale tensor, at `page`, `row` of a KV head.
+__device__ __forceinline__ long long kv_row(const KvMap& m, int head, int page, int row) {
+  return (static_cast<long long>(page) * m.page_size + row) * m.Hkv + head;
+}
+__device__ __forceinline__ long long kv_scale(const KvMap& m, int head, int page, int row) {
+  return (static_cast<long long>(page) * m.Hkv + head) * m.page_size + row;
+}
+
+__device__ __forceinline__ long long shfl64(long long x, int from) {
+  const uint32_t lo = __shfl_sync(0xffffffffu, static_cast<uint32_t>(x), from);
+  const uint32_t hi = __shfl_sync(0xffffffffu, static_cast<uint32_t>(x >> 32), from);
+  return static_cast<long long>(static_cast<unsigned long long>(hi) << 32 | lo);
+}
+
 // The first block reports token offsets that do not start at 0, do not ascend, or pass N.
 __device__ __forceinline__ void kv_check_cu(const KvMap& m) {
   if (m.cu_tokens == nullptr || blockIdx.x != 0) return;
@@ -193,6 +207,7 @@ __global__ void __launch_bounds__(256) fa_kv_write_kernel(const KvCopyParams p) 
   load(0);  // (on its way while the places are looked up)
   int page = -1, row = 0;  // of token tok0 + lane
   if (lane < left) kv_locate<kPaged>(map, static_cast<int>(tok0) + lane, page, row);
+  const long long at = page < 0 ? -1 : kv_row(map, head, page, row);
   float my_scale = 0.f;
 #pragma unroll 1
   for (int s0 = 0; s0 < kSteps; s0 += kU) {
@@ -224,8 +239,7 @@ __global__ void __launch_bounds__(256) fa_kv_write_kernel(const KvCopyParams p) 
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int r = (s0 + u) * kRows + lane / kLanes;
-      const int pg = __shfl_sync(0xffffffffu, page, r & 31);
-      const int rw = __shfl_sync(0xffffffffu, row, r & 31);
+      const long long to = shfl64(at, r & 31);
       const float inv_u = __shfl_sync(0xffffffffu, inv, lane / kLanes * kLanes + u);
       const float ns_u = -__shfl_sync(0xffffffffu, base, lane / kLanes * kLanes + u);
       uint2 c0, c1;
@@ -238,15 +252,15 @@ __global__ void __launch_bounds__(256) fa_kv_write_kernel(const KvCopyParams p) 
         c1 = kv_codes8<kBits, true>(w[u][1], inv_u, ns_u, f_u);
       }
       if (inv_u == 0.f) c0 = c1 = make_uint2(0, 0);
-      if (pg >= 0) {
-        uint8_t* dst = codes + ((static_cast<size_t>(pg) * map.page_size + rw) * map.Hkv + head) * kRow;
+      if (to >= 0) {
+        uint8_t* dst = codes + to * kRow;
         kv_store8<kBits>(dst + kBits * l, c0);
         kv_store8<kBits>(dst + kRow / 2 + kBits * l, c1);
       }
     }
   }
   if (page >= 0)
-    scales[(static_cast<size_t>(page) * map.Hkv + head) * map.page_size + row] = my_scale;
+    scales[kv_scale(map, head, page, row)] = my_scale;
 }
 
 // 8 codes -> bf16(code * scale).
@@ -297,17 +311,16 @@ __global__ void __launch_bounds__(256) fa_kv_read_kernel(const KvCopyParams p) {
   int page = -1, row = 0;
   if (lane < left) kv_locate<kPaged>(map, static_cast<int>(tok0) + lane, page, row);
   const float my_scale =
-      page >= 0 ? scales[(static_cast<size_t>(page) * map.Hkv + head) * map.page_size + row] : 0.f;
+      page >= 0 ? scales[kv_scale(map, head, page, row)] : 0.f;
+  const long long at = page < 0 ? -1 : kv_row(map, head, page, row);
   const int l = lane % kLanes;
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     const int r = s * kRows + lane / kLanes;
-    const int pg = __shfl_sync(0xffffffffu, page, r);
-    const int rw = __shfl_sync(0xffffffffu, row, r);
+    const long long from = shfl64(at, r);
     const float scale = __shfl_sync(0xffffffffu, my_scale, r);
-    if (pg >= 0) {
-      const uint8_t* src =
-          codes + ((static_cast<size_t>(pg) * map.page_size + rw) * map.Hkv + head) * kRow;
+    if (from >= 0) {
+      const uint8_t* src = codes + from * kRow;
       uint4* dst = reinterpret_cast<uint4*>(out + ((tok0 + r) * map.Hkv + head) * D);
       dst[l] = kv_values8<kBits>(src + kBits * l, scale);
       dst[l + kLanes] = kv_values8<kBits>(src + kRow / 2 + kBits * l, scale);
