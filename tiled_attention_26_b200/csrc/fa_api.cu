@@ -669,7 +669,7 @@ template <int D, int kBits, bool kPaged, bool kWrite, int kTokens>
 int launch_kv_copy_tokens(const fa::KvCopyParams& p, cudaStream_t stream) {
   const long long units = (static_cast<long long>(p.map.N) + kTokens - 1) / kTokens * 2 * p.map.Hkv;
   const long long grid = (units + 7) / 8;
-  if (grid > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  if (8 * grid > 0xffffffffLL) return FA_ERR_INVALID_ARG;
   if (kWrite)
     fa::fa_kv_write_kernel<D, kBits, kPaged, kTokens><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
   else

@@ -177,11 +177,11 @@ __global__ void __launch_bounds__(256) fa_kv_write_kernel(const KvCopyParams p) 
   constexpr float m = kBits == 8 ? 127.f : 7.f;
   const KvMap& map = p.map;
   const int lane = threadIdx.x & 31;
-  const long long unit = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int head = static_cast<int>(unit % map.Hkv);
-  const long long rest = unit / map.Hkv;
+  const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);  // (fewer than 2^32: the launch checks)
+  const int head = static_cast<int>(unit % static_cast<uint32_t>(map.Hkv));
+  const uint32_t rest = unit / static_cast<uint32_t>(map.Hkv);
   const bool is_v = rest & 1;
-  const long long tok0 = (rest >> 1) * kTokens;
+  const long long tok0 = static_cast<long long>(rest >> 1) * kTokens;
   if constexpr (kPaged) kv_check_cu(map);
   if (tok0 >= map.N) return;
   const long long stride = is_v ? p.v_stride : p.k_stride;
@@ -297,11 +297,11 @@ __global__ void __launch_bounds__(256) fa_kv_read_kernel(const KvCopyParams p) {
   const KvMap& map = p.map;
   if constexpr (kPaged) kv_check_cu(map);
   const int lane = threadIdx.x & 31;
-  const long long unit = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int head = static_cast<int>(unit % map.Hkv);
-  const long long rest = unit / map.Hkv;
+  const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);  // (fewer than 2^32: the launch checks)
+  const int head = static_cast<int>(unit % static_cast<uint32_t>(map.Hkv));
+  const uint32_t rest = unit / static_cast<uint32_t>(map.Hkv);
   const bool is_v = rest & 1;
-  const long long tok0 = (rest >> 1) * kTokens;
+  const long long tok0 = static_cast<long long>(rest >> 1) * kTokens;
   if (tok0 >= map.N) return;
   const int left = static_cast<int>(min(static_cast<long long>(kTokens), map.N - tok0));
   const uint8_t* codes = is_v ? p.v_codes : p.k_codes;
