@@ -79,3 +79,19 @@ def test_backward_kernels_fit_one_cta(kernels):
     for name, v in found.items():
         assert v["regs"] * 320 <= REGFILE, (name, v)
         assert v["spill"] <= 16, (name, v)  # (D = 64 keeps one 8-byte value in local memory)
+
+
+def test_shared_prefix_launch_registers_match_the_warpgroup_split(kernels):
+    # 512 threads at 128 registers: two softmax warpgroups of 192, dequantisation 72, the rest 56
+    found = _select(kernels, "_ZN2fa23fa_shared_prefix_kernelI")
+    assert len(found) == 8, sorted(found)  # D, bits, streams or row blocks
+    for name, v in found.items():
+        assert v["regs"] == 128, (name, v)
+        assert v["spill"] <= 48, (name, v)
+
+
+def test_decode_16_row_kernels_fit_two_ctas_per_sm(kernels):
+    # 5 warps a CTA, two CTAs: up to 3 warps on a quarter of the register file
+    for name, v in _select(kernels, "_ZN2fa24fa_decode_split16_kernelI").items():
+        assert v["regs"] * 32 * 3 <= REGFILE // 4, (name, v)
+        assert v["spill"] <= 32, (name, v)

@@ -240,7 +240,8 @@ __device__ __forceinline__ uint32_t nib_hi16_f16x2(uint32_t raw) {
 }
 
 // The split kernel for kHB blocks of 8 query heads per CTA: with two, both use each converted K and V
-// fragment, which is most of the work.
+// fragment, which is most of the work (131072 keys x 8 KV heads of 128 dims, 16 rows: 62 us, 4.4 TB/s; two
+// CTAs of 8 rows each took 81).  Three CTAs per SM instead of two spill and take 75.
 template <int D, bool kPaged, int kBits, int kHB>
 __device__ __forceinline__ void decode_split(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                              const DecodeParams& p) {

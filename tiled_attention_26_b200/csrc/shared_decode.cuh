@@ -8,28 +8,38 @@
 // (the codes take part without being decompressed first: "Flash Attention on Ascend: three
 // techniques", section 3).  The keys each sequence owns go through the paged split kernel of
 // decode.cuh; both write partial outputs with their log-sum-exp, and fa_decode_combine_kernel
-// merges them: L = log sum_s exp(L_s), O = sum_s exp(L_s - L) O_s.
+// merges them: L = log sum_s exp(L_s), O = sum_s exp(L_s - L) O_s.  (For few rows or a short prefix the
+// prefix goes through the split kernel as well, as one sequence of R rows: the launch decides.)
 //
 // fa_shared_prefix_kernel, one CTA per (KV head, block of rows, split of the prefix), 512 threads:
 //   warps 0-3   softmax of S tile 0 (thread = query row = TMEM lane), warps 4-7 of S tile 1
 //   warps 8-11  dequantisation: thread = key; K codes to fp16 (exact), V codes times their scale to
 //               fp16, both into the swizzled layout the tensor core reads
 //   warp 12     TMA producer: K and V code tiles of 128 keys, one box per page piece
-//   warp 14     the keys' scales, and the exponent E below
-//   warp 13     allocates TMEM and issues tcgen05.mma from one thread: S_t = Q_t K^T,
-//               O_t += P_t V with P_t from TMEM;  warp 15 idles
+//   warp 13     allocates TMEM and issues tcgen05.mma from one lane: S_t = Q_t K^T,
+//               O_t += P_t V with P_t from TMEM
+//   warp 14     the keys' scales, and the exponent E below;  warp 15 idles
 // The two S tiles are two blocks of 128 query rows that share every K/V tile (kStream = false), or,
 // when R <= 128, two interleaved streams of key tiles over one block of rows (kStream = true), merged
-// in shared memory at the end; either way one tile's softmax runs while the tensor core works on
-// the other.
+// as they are written; either way one tile's softmax runs while the tensor core works on the other.
+//
+// What bounds it: neither memory nor the tensor core but the chain of one tile - its softmax, then its
+// P V and its next Q K^T, before which the next softmax cannot start (P lies over S).  With two
+// tiles of 128 x 128 scores at D = 128, 4.6 thousand cycles a pair, of which a softmax warp computes 3.2 (exponentials 1.7,
+// scaling and maximum 0.6) and the tensor core 2.05; 32768 keys x 64 sequences x 32 / 8 heads 54 us, 640 TFLOP/s
+// (B200).  Two things cost most on the way there: the unrolled code of all roles in the instruction
+// caches, hence the rolled loops wherever registers allow, and operands of tcgen05.mma in vector registers,
+// hence the converged MMA warp.
+// A single accumulator with three buffers of S, which lets S run ahead of the softmax, is no faster: the
+// registers and the converted tiles that it needs per row are twice as many.
 //
 // Number formats.  Q is scaled per row by a power of two and kept in fp16, which holds a bf16 row
-// exactly (elements more than 2^29 below the row's largest lose bits).  Scores, maxima, sums, O and
-// log-sum-exps are fp32; k_scale multiplies the fp32 scores, so QK^T has no rounding of its
-// own.  P = 2^7 p (p <= 2^8 with the lazy maximum) and v_scale * vcode * 2^E are rounded to fp16
-// (relative 2^-11 each, an eighth of the bf16 output's): the shift by 2^7 keeps weights down to
-// 2^-31 of the maximum from vanishing, and the power E, lowered (with an exact rescale of O) when a
-// larger v_scale arrives, keeps V below 2^15.
+// exactly (elements more than 2^29 below the row's largest lose bits, 2^25 for INT4).  Scores, maxima,
+// sums, O and log-sum-exps are fp32; k_scale multiplies the fp32 scores, so QK^T has no rounding
+// of its own.  P = 2^7 p (p <= 2^8 with the lazy maximum), v_scale * 2^E and its product with the code
+// are rounded to fp16 (relative 2^-11 each, an eighth of the bf16 output's): the shift by 2^7 keeps
+// weights down to 2^-31 of the maximum from vanishing, and the power E, lowered (with an exact rescale
+// of O) when a larger v_scale arrives, keeps V below 2^15.
 #pragma once
 
 #include "decode.cuh"
