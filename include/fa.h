@@ -375,8 +375,9 @@ FA_API int fa_kv_gather_int4_paged(const uint8_t* k_pages, const uint8_t* v_page
  *                 the prefix; a length may be 0.  A sequence that sees no key at all gets O = 0 and
  *                 LSE = -inf.
  *   max_prefix_pages, max_pages_per_seq  times page_size at most 2^30 each.
- *   num_splits    splits of the own keys as for fa_decode_int8_paged, or 0: the library chooses.  How
- *                 the prefix is split follows from the sizes.
+ *   num_splits    splits of the own keys as for fa_decode_int8_paged, or 0: the library chooses (no
+ *                 piece smaller than 512 keys).  How the prefix is split, and the kernel that reads it,
+ *                 follow from the sizes given here, not from prefix_len.
  *   workspace     at least fa_decode_shared_workspace_bytes(B, Hq, Hkv, D, max_prefix_pages *
  *                 page_size, max_pages_per_seq * page_size, num_splits) bytes, 16-byte aligned;
  *                 contents on entry do not matter.  Calls that may run at the same time must not

@@ -191,6 +191,8 @@ CONTIGUOUS = [  # B, S, Hkv, D, kind
     (3, 31, 5, 64, "ties"), (2, 70, 2, 128, "ties"), (2, 65, 2, 128, "ties4"),
     (1, 40, 2, 64, "huge"), (2, 64, 3, 128, "tiny"), (1, 32, 2, 64, "zeros"),
     (2, 35, 4, 128, "nonfinite"), (1, 4097, 8, 128, "normal"),
+    # enough rows for 32 tokens a warp (37888)
+    (2, 3001, 8, 128, "normal"), (3, 2543, 5, 64, "ties"), (1, 12701, 3, 64, "tiny"), (2, 9501, 2, 128, "nonfinite"),
 ]
 
 
@@ -242,6 +244,9 @@ PAGED = [  # bits, Hkv, D, P, history, new tokens, padding rows
     (4, 2, 128, 16, [9, 3, 0], [0, 129, 0], 2),
     (4, 5, 64, 64, [63, 1], [2, 300], 0),
     (8, 1, 128, 256, [0, 0, 0, 0, 255], [0, 0, 257, 0, 1], 31),
+    # enough rows for 32 tokens a warp (37888)
+    (8, 8, 128, 64, [5, 0, 100, 7, 63], [1700, 0, 33, 2900, 401], 3),
+    (4, 5, 64, 16, [9 * b for b in range(37)], [(613 * b) % 420 for b in range(37)], 40),
 ]
 
 
@@ -443,3 +448,44 @@ def test_decode_of_a_row_written_from_nan_is_nan(built, bits, S, splits):
         o[1, 0, 4:8], lse[1, 4:8] = 0, 0
         assert torch.isfinite(o).all() and torch.isfinite(lse).all()
         x[1, 2, 1] = kept
+
+
+@gpu
+@pytest.mark.parametrize("bits", [8, 4])
+def test_with_a_stream_as_without(built, bits):
+    """The calls made directly (no stream argument) and those that go through the Python checks agree."""
+    import torch
+    here = torch.cuda.current_stream()
+    k, v = (_bf16(make_rows(s, (2, 70, 3, 64), "normal")) for s in (1, 2))
+    a, b = _call("quantize", bits)(k, v), _call("quantize", bits)(k, v, stream=here)
+    a += _call("dequantize", bits)(*a)
+    b += _call("dequantize", bits)(*b, stream=here)
+    B, n, bt, pool, x, cu, dev = _paged_case(bits, 3, 64, 16, [3, 0, 40], [20, 1, 9], 2)
+    twin = [t.clone() for t in dev["pool"]]
+    _call("append", bits, True)(*dev["x"], *dev["pool"], dev["bt"], dev["pos"], dev["cu"])
+    _call("append", bits, True)(*dev["x"], *twin, dev["bt"], dev["pos"], dev["cu"], stream=here)
+    a += tuple(dev["pool"]) + _call("gather", bits, True)(*dev["pool"], dev["bt"], 30, dev["pos"], dev["cu"])
+    b += tuple(twin) + _call("gather", bits, True)(*twin, dev["bt"], 30, dev["pos"], dev["cu"], stream=here)
+    for s, t in zip(a, b):
+        assert s.dtype == t.dtype and s.shape == t.shape and torch.equal(s, t)
+
+
+@gpu
+def test_refusals_on_the_gpu(built):
+    """What the direct calls leave to the Python checks is refused there, and nothing is launched."""
+    import torch
+    B, n, bt, pool, x, cu, dev = _paged_case(8, 2, 64, 16, [3], [20], 0)
+    args = [*dev["x"], *dev["pool"], dev["bt"], dev["pos"], dev["cu"]]
+    for i, bad, err in ((0, dev["x"][0].float(), TypeError), (1, dev["x"][1][:, :1], ValueError),
+                        (2, dev["pool"][0].view(torch.uint8), TypeError), (4, dev["pool"][2].transpose(1, 2), ValueError),
+                        (6, dev["bt"].cpu(), ValueError), (7, dev["pos"].long(), TypeError),
+                        (8, dev["cu"][:1], ValueError)):
+        with pytest.raises(err):
+            fa.fa_kv_append_int8_paged(*args[:i], bad, *args[i + 1:])
+    with pytest.raises(fa.FaError):  # rows of 96 dims
+        fa.fa_kv_quantize_int8(*[torch.zeros(1, 4, 2, 96, dtype=torch.bfloat16, device="cuda")] * 2)
+    with pytest.raises(fa.FaError):  # 16-byte alignment
+        odd = torch.zeros(4 * 2 * 64 + 4, dtype=torch.bfloat16, device="cuda")[4:].view(1, 4, 2, 64)
+        fa.fa_kv_quantize_int8(odd, odd)
+    for got, w in zip(dev["pool"], pool):
+        assert np.array_equal(got.cpu().numpy(), w)

@@ -200,6 +200,10 @@ CASES = [  # bits, B, Hq, Hkv, D, P, prefix, own lengths, num_splits
     (8, 40, 8, 2, 64, 64, 0, [b % 3 for b in range(40)], 0),
     (4, 2, 8, 2, 128, 64, 300, [0, 0], 0),
     (8, 130, 4, 2, 64, 16, 50, [b % 20 for b in range(130)], 0),
+    # more pages in one split than the kernel stages (256); 16 rows a CTA
+    (8, 2, 4, 1, 64, 16, 40, [5000, 3], 1),
+    (4, 1, 16, 1, 128, 16, 20, [4700], 1),
+    (8, 2, 29, 1, 128, 32, 4500, [0, 700], 2),
 ]
 
 
@@ -430,3 +434,27 @@ def test_two_streams_at_once(built):
         (c if i % 2 == 0 else e).check(o, lse) if i < 2 else None
         assert torch.equal(o, outs[i % 2][0]) and torch.equal(lse, outs[i % 2][1])
     assert fa.fa_device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("bits", [8, 4])
+def test_given_buffers_and_a_stream_change_nothing(built, bits):
+    import torch
+    c = Case(bits, 3, 12, 2, 64, 16, 100, [20, 0, 33])
+    o, lse = c.call()
+    o2, none = c.call(return_lse=False)
+    assert none is None and torch.equal(o, o2)
+    out = dict(o=torch.empty_like(o), lse=torch.empty_like(lse),
+               workspace=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+    o3, lse3 = c.call(**out)
+    assert o3.data_ptr() == out["o"].data_ptr() and torch.equal(o, o3) and torch.equal(lse, lse3)
+    o4, lse4 = c.call(stream=torch.cuda.current_stream())
+    assert torch.equal(o, o4) and torch.equal(lse, lse4)
+    with pytest.raises(fa.FaError):
+        c.call(workspace=out["workspace"][:1000])
+    with pytest.raises(fa.FaError):
+        c.call(workspace=out["workspace"][8:])
+    with pytest.raises(ValueError, match="workspace"):
+        c.call(workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="lse"):
+        c.call(lse=lse.flatten())
