@@ -95,3 +95,12 @@ def test_decode_16_row_kernels_fit_two_ctas_per_sm(kernels):
     for name, v in _select(kernels, "_ZN2fa24fa_decode_split16_kernelI").items():
         assert v["regs"] * 32 * 3 <= REGFILE // 4, (name, v)
         assert v["spill"] <= 32, (name, v)
+
+
+def test_decode_pair_kernels_fit_as_the_single_ones(kernels):
+    for name, v in _select(kernels, "_ZN2fa21fa_decode_pair_kernelI").items():
+        if "ELi1EE" in name:  # 8 rows a CTA
+            assert v["regs"] * 160 * 3 <= REGFILE, (name, v)
+        else:
+            assert v["regs"] * 32 * 3 <= REGFILE // 4, (name, v)
+        assert v["spill"] <= 32, (name, v)

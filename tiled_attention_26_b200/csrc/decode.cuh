@@ -244,7 +244,7 @@ __device__ __forceinline__ uint32_t nib_hi16_f16x2(uint32_t raw) {
 // CTAs of 8 rows each took 81).  Three CTAs per SM instead of two spill and take 75.
 template <int D, bool kPaged, int kBits, int kHB>
 __device__ __forceinline__ void decode_split(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                             const DecodeParams& p) {
+                                             const DecodeParams& p, int seq_block) {
   using C = DecodeCfg<D, kBits, kHB>;
   constexpr int KS = D / 16;            // QK k-steps
   constexpr int MT = D / 16;            // PV m-tiles (16 output dims each)
@@ -273,8 +273,8 @@ __device__ __forceinline__ void decode_split(const CUtensorMap& tm_k, const CUte
   // same time stream the same key rows (all KV heads of a key are contiguous in memory).
   const int kvh = blockIdx.x, split = blockIdx.y;
   const int nhb = (p.G + 8 * kHB - 1) / (8 * kHB);
-  int b = static_cast<int>(blockIdx.z) / nhb;
-  const int hb = static_cast<int>(blockIdx.z) % nhb * kHB;
+  int b = seq_block / nhb;
+  const int hb = seq_block % nhb * kHB;
   if constexpr (kPaged) {
     // Longest sequences first: with mixed lengths a split's work is proportional to its
     // sequence's length, and CTAs start in grid order, so the long ones go in the first wave
@@ -805,7 +805,7 @@ template <int D, bool kPaged, int kBits>
 __global__ void __launch_bounds__(160, kBits == 8 ? 3 : 1) fa_decode_split_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const DecodeParams p) {
-  decode_split<D, kPaged, kBits, 1>(tm_k, tm_v, p);
+  decode_split<D, kPaged, kBits, 1>(tm_k, tm_v, p, static_cast<int>(blockIdx.z));
 }
 
 // Two blocks of 8 query heads per CTA, over a paged cache.
@@ -813,7 +813,23 @@ template <int D, int kBits>
 __global__ void __launch_bounds__(160, 2) fa_decode_split16_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const DecodeParams p) {
-  decode_split<D, true, kBits, 2>(tm_k, tm_v, p);
+  decode_split<D, true, kBits, 2>(tm_k, tm_v, p, static_cast<int>(blockIdx.z));
+}
+
+// Two calls over one cache in one launch: blocks of grid z from first_z on belong to the second.
+struct DecodePair {
+  DecodeParams p[2];
+  int first_z;
+};
+template <int D, int kBits, int kHB>
+__global__ void __launch_bounds__(160, kHB == 1 ? 3 : 2) fa_decode_pair_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const __grid_constant__ DecodePair pair) {
+  const int z = static_cast<int>(blockIdx.z);
+  const bool second = z >= pair.first_z;
+  const DecodeParams& p = pair.p[second ? 1 : 0];
+  if (static_cast<int>(blockIdx.y) >= p.splits) return;  // the grid has the larger number of splits
+  decode_split<D, true, kBits, kHB>(tm_k, tm_v, p, second ? z - pair.first_z : z);
 }
 
 // Merge kernel: kWarps warps per (batch, query head), 4 warps a block.  A warp takes every kWarps-th

@@ -381,6 +381,25 @@ int launch_split_rows(const CodeMaps& maps, const fa::DecodeParams& p, bool depe
                  : launch_split<D, true, kBits>(maps, p, dependent, stream);
 }
 
+// Two calls over one cache in one launch.
+std::atomic<uint64_t> g_attr_pair[8];
+template <int D, int kBits, int kHB>
+int launch_pair(const CodeMaps& maps, const fa::DecodeParams& a, const fa::DecodeParams& b,
+                cudaStream_t stream) {
+  using C = fa::DecodeCfg<D, kBits, kHB>;
+  const long long za = static_cast<long long>(a.B) * ((a.G + 8 * kHB - 1) / (8 * kHB));
+  const long long z = za + static_cast<long long>(b.B) * ((b.G + 8 * kHB - 1) / (8 * kHB));
+  const int splits = std::max(a.splits, b.splits);
+  if (splits > 65535 || z > 65535) return FA_ERR_INVALID_ARG;
+  auto kernel = fa::fa_decode_pair_kernel<D, kBits, kHB>;
+  constexpr int variant = (D == 128 ? 4 : 0) + (kBits == 4 ? 2 : 0) + kHB - 1;
+  const int rc = ensure_smem_attr(kernel, C::kSmemBytes, g_attr_pair[variant]);
+  if (rc != FA_OK) return rc;
+  fa::DecodePair pair{{a, b}, static_cast<int>(za)};
+  return launch(kernel, dim3(a.Hkv, splits, static_cast<unsigned>(z)), 160, C::kSmemBytes, false,
+                stream, maps.k, maps.v, pair);
+}
+
 // Merge of `splits` partials: a programmatic dependent that waits on the device for them.
 template <int D, int kWarps>
 int launch_combine(const fa::DecodeParams& p, int splits, void* o, float* lse, cudaStream_t stream) {
@@ -560,15 +579,20 @@ bool shared_through_split(int D, long long R, int Hkv, long long max_keys) {
   return split_blocks(R) * T < (D == 128 ? 1.45 : 2.2) * tile * T + 4.0;
 }
 
-// Splits of the prefix.  Through the split kernel: what fills the GPU with its CTAs.  Otherwise one CTA per
+// Splits of the prefix.  Through the split kernel: what its CTAs find room for beside those
+// of the own keys.  Otherwise one CTA per
 // SM runs a split of one (KV head, row block) in about (tiles + 3) tile times (start-up, epilogue and
 // its share of the merge count for three), in as many waves as the CTAs need; the split count with
 // the least total time, the smaller of equals.
-int shared_prefix_splits(int D, int B, int Hq, int Hkv, long long max_keys) {
+int shared_prefix_splits(int D, int B, int Hq, int Hkv, long long max_keys, int own_splits) {
   const long long R = static_cast<long long>(B) * (Hq / Hkv);
   const long long tiles = std::max(1ll, (max_keys + 127) / 128);
-  if (shared_through_split(D, R, Hkv, max_keys))
-    return static_cast<int>(std::min(tiles, std::max(1ll, split_slots(R) / (Hkv * split_blocks(R)))));
+  if (shared_through_split(D, R, Hkv, max_keys)) {
+    const long long slots = split_slots(R);
+    const long long own = static_cast<long long>(B) * Hkv * split_blocks(Hq / Hkv) * own_splits;
+    return static_cast<int>(std::min(
+        tiles, std::max(1ll, (slots - std::min(own, slots / 2)) / (Hkv * split_blocks(R)))));
+  }
   const long long base = static_cast<long long>(Hkv) * (R <= 128 ? 1 : (R + 255) / 256);
   int best = 1;
   long long best_cost = -1;
@@ -630,8 +654,8 @@ int launch_shared(const fa::DecodeParams& own, const fa::SharedParams& sp, void*
   int rc = encode_codes(&maps, own.k, own.v, D * kBits / 8, own.Hkv, 1 << own.page_shift,
                         own.num_pages, true);
   if (rc != FA_OK) return rc;
-  if ((rc = launch_split_rows<D, kBits>(maps, own, false, stream)) != FA_OK) return rc;
-  if (shared_through_split(D, sp.R, sp.Hkv, static_cast<long long>(sp.max_pages) << sp.page_shift)) {
+  const long long max_prefix = static_cast<long long>(sp.max_pages) << sp.page_shift;
+  if (shared_through_split(D, sp.R, sp.Hkv, max_prefix)) {
     fa::DecodeParams pre = own;  // one sequence of R rows
     pre.B = 1;
     pre.G = sp.R;
@@ -642,11 +666,20 @@ int launch_shared(const fa::DecodeParams& own, const fa::SharedParams& sp, void*
     pre.min_chunk = fa::kDecodeMinChunk;
     pre.o_part = sp.o_part;
     pre.lse_part = sp.lse_part;
-    rc = launch_split_rows<D, kBits>(maps, pre, true, stream);
-  } else if (sp.R <= 128) {
-    rc = launch_shared_prefix<D, kBits, true>(maps, sp, stream);
+    // one launch where both want the same number of rows a CTA
+    if (sp.R <= 8) {
+      rc = launch_pair<D, kBits, 1>(maps, own, pre, stream);
+    } else if (own.G > 8) {
+      rc = launch_pair<D, kBits, 2>(maps, own, pre, stream);
+    } else {
+      rc = launch_split<D, true, kBits>(maps, own, false, stream);
+      if (rc == FA_OK) rc = launch_split16<D, kBits>(maps, pre, true, stream);
+    }
   } else {
-    rc = launch_shared_prefix<D, kBits, false>(maps, sp, stream);
+    rc = launch_split_rows<D, kBits>(maps, own, false, stream);
+    if (rc == FA_OK)
+      rc = sp.R <= 128 ? launch_shared_prefix<D, kBits, true>(maps, sp, stream)
+                       : launch_shared_prefix<D, kBits, false>(maps, sp, stream);
   }
   if (rc != FA_OK) return rc;
   // four warps per row where one per row leaves the GPU idle over many partials
@@ -776,7 +809,7 @@ bool shared_splits(int B, int Hq, int Hkv, int D, long long max_prefix, long lon
     return false;
   if (static_cast<long long>(B) * Hq > 0x7fffffffLL) return false;
   *own = num_splits > 0 ? num_splits : shared_own_splits(B, Hq, Hkv, max_own);
-  *prefix = shared_prefix_splits(D, B, Hq, Hkv, max_prefix);
+  *prefix = shared_prefix_splits(D, B, Hq, Hkv, max_prefix, *own);
   return *own <= 65535;
 }
 
