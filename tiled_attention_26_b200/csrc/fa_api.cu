@@ -579,26 +579,30 @@ bool shared_through_split(int D, long long R, int Hkv, long long max_keys) {
   return split_blocks(R) * T < (D == 128 ? 1.45 : 2.2) * tile * T + 4.0;
 }
 
-// Splits of the prefix.  Through the split kernel: what its CTAs find room for beside those
-// of the own keys.  Otherwise one CTA per
-// SM runs a split of one (KV head, row block) in about (tiles + 3) tile times (start-up, epilogue and
-// its share of the merge count for three), in as many waves as the CTAs need; the split count with
-// the least total time, the smaller of equals.
+// Splits of the prefix: the count with the least estimate of tile times, the smaller of equals.  A split
+// costs the merge 0.057 us, 1/17 of the split kernel's tile or 1/25 of the tcgen05 kernel's (one KV head,
+// 8 rows, 32768 keys: 256 / 128 / 64 splits 23 / 16.5 / 14.5 us).  Through the split kernel as many as
+// its CTAs find room for beside those of the own keys.  Otherwise one CTA per SM runs a split of one (KV head,
+// row block) in about (tiles + 3) tile times (start-up and epilogue count for three), in as many
+// waves as the CTAs need.
 int shared_prefix_splits(int D, int B, int Hq, int Hkv, long long max_keys, int own_splits) {
   const long long R = static_cast<long long>(B) * (Hq / Hkv);
   const long long tiles = std::max(1ll, (max_keys + 127) / 128);
-  if (shared_through_split(D, R, Hkv, max_keys)) {
+  const bool few = shared_through_split(D, R, Hkv, max_keys);
+  const long long base = Hkv * (few ? split_blocks(R) : R <= 128 ? 1 : (R + 255) / 256);
+  long long limit = kSms;
+  if (few) {
     const long long slots = split_slots(R);
     const long long own = static_cast<long long>(B) * Hkv * split_blocks(Hq / Hkv) * own_splits;
-    return static_cast<int>(std::min(
-        tiles, std::max(1ll, (slots - std::min(own, slots / 2)) / (Hkv * split_blocks(R)))));
+    limit = std::max(1ll, (slots - std::min(own, slots / 2)) / base);
   }
-  const long long base = static_cast<long long>(Hkv) * (R <= 128 ? 1 : (R + 255) / 256);
   int best = 1;
-  long long best_cost = -1;
-  for (int s = 1; s <= kSms && s <= tiles; ++s) {
-    const long long cost = (base * s + kSms - 1) / kSms * ((tiles + s - 1) / s + 3);
-    if (best_cost < 0 || cost < best_cost) {
+  double best_cost = -1.0;
+  for (int s = 1; s <= limit && s <= tiles; ++s) {
+    const double per = static_cast<double>((tiles + s - 1) / s);
+    const double cost = few ? per + s / 17.0
+                            : static_cast<double>((base * s + kSms - 1) / kSms) * (per + 3.0) + s / 25.0;
+    if (best_cost < 0.0 || cost < best_cost) {
       best = s;
       best_cost = cost;
     }
