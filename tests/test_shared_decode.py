@@ -458,3 +458,19 @@ def test_given_buffers_and_a_stream_change_nothing(built, bits):
         c.call(workspace=torch.empty(1 << 20, dtype=torch.uint8))
     with pytest.raises(ValueError, match="lse"):
         c.call(lse=lse.flatten())
+
+
+@gpu
+@pytest.mark.parametrize("wide", [False, True])
+def test_one_workspace_for_different_calls_in_a_row(built, wide):
+    """Calls of different inputs that follow each other on one stream, in one workspace: none sees the partials
+    of another."""
+    import torch
+    shape = (8, 16, 480, 30, 128, 64, 600) if wide else (8, 16, 16, 2, 128, 64, 3000)
+    cases = [Case(*shape, [(37 * b + 50 * i) % 300 for b in range(16)], seed=40 + i) for i in range(3)]
+    ref = [c.call() for c in cases]
+    cases[0].check(*ref[0])
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    outs = [cases[i % 3].call(workspace=ws) for i in range(60)]
+    for i, (o, lse) in enumerate(outs):
+        assert torch.equal(o, ref[i % 3][0]) and torch.equal(lse, ref[i % 3][1]), i

@@ -735,9 +735,13 @@ __device__ __forceinline__ void decode_split(const CUtensorMap& tm_k, const CUte
     if (lane == 0) mbar_arrive(bar_empty(s));
   }
 
-  // Where this grid was launched as a programmatic dependent, it does not end before the grid it
-  // depends on: whoever waits for this one then waits for both.
-  if constexpr (kPaged) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Where this grid was launched as a programmatic dependent (of a kernel whose results it does not
+  // read), it does not end before that one does, for one CTA waits: whoever waits for this grid then waits
+  // for both.
+  if constexpr (kPaged) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
 
   // ---- merge the 4 warps, 8 heads at a time (the stage tiles are free now: every stage has been
   // consumed) ----

@@ -584,24 +584,31 @@ bool shared_through_split(int D, long long R, int Hkv, long long max_keys) {
 // 8 rows, 32768 keys: 256 / 128 / 64 splits 23 / 16.5 / 14.5 us).  Through the split kernel as many as
 // its CTAs find room for beside those of the own keys.  Otherwise one CTA per SM runs a split of one (KV head,
 // row block) in about (tiles + 3) tile times (start-up and epilogue count for three), in as many
-// waves as the CTAs need.
-int shared_prefix_splits(int D, int B, int Hq, int Hkv, long long max_keys, int own_splits) {
+// waves as the CTAs need on the SMs that it leaves to the own keys' kernel: their share of the work, a
+// CTA of own keys a third of an SM for 4.5 us and 1.1 us a stage (half of the longest sequence).
+int shared_prefix_splits(int D, int B, int Hq, int Hkv, long long max_keys, int own_splits,
+                         long long max_own) {
   const long long R = static_cast<long long>(B) * (Hq / Hkv);
   const long long tiles = std::max(1ll, (max_keys + 127) / 128);
   const bool few = shared_through_split(D, R, Hkv, max_keys);
   const long long base = Hkv * (few ? split_blocks(R) : R <= 128 ? 1 : (R + 255) / 256);
-  long long limit = kSms;
+  const long long own = static_cast<long long>(B) * Hkv * split_blocks(Hq / Hkv) * own_splits;
+  long long limit = kSms, sms = kSms;
   if (few) {
     const long long slots = split_slots(R);
-    const long long own = static_cast<long long>(B) * Hkv * split_blocks(Hq / Hkv) * own_splits;
     limit = std::max(1ll, (slots - std::min(own, slots / 2)) / base);
+  } else {
+    const double stages = std::max(1.0, 0.5 / 128 * max_own / own_splits);
+    const double own_time = own * (4.5 + 1.1 * stages) / 3;
+    const double time = base * tiles * (R <= 128 ? 1.4 : 2.5) + 9.0 * kSms;
+    sms -= std::min<long long>(kSms / 5, static_cast<long long>(kSms * own_time / (own_time + time) + 0.5));
   }
   int best = 1;
   double best_cost = -1.0;
   for (int s = 1; s <= limit && s <= tiles; ++s) {
     const double per = static_cast<double>((tiles + s - 1) / s);
     const double cost = few ? per + s / 17.0
-                            : static_cast<double>((base * s + kSms - 1) / kSms) * (per + 3.0) + s / 25.0;
+                            : static_cast<double>((base * s + sms - 1) / sms) * (per + 3.0) + s / 25.0;
     if (best_cost < 0.0 || cost < best_cost) {
       best = s;
       best_cost = cost;
@@ -645,12 +652,12 @@ int launch_shared_prefix(const CodeMaps& maps, const fa::SharedParams& p, cudaSt
     g_shared_regs[variant].store(regs, std::memory_order_release);
   }
   if (regs < C::kLaunchRegs) return FA_ERR_UNSUPPORTED;
-  return launch(kernel, dim3(static_cast<unsigned>(grid)), C::kThreads, C::kSmemBytes, true, stream,
+  return launch(kernel, dim3(static_cast<unsigned>(grid)), C::kThreads, C::kSmemBytes, false, stream,
                 maps.k, maps.v, p);
 }
 
-// The own keys' partials, beside them (a programmatic dependent that reads nothing of it, and does not
-// end before it) the prefix's, then the merge of both.
+// The partials of the own keys and of the prefix, one kernel beside the other (a programmatic dependent
+// that reads nothing of it, and does not end before it), then the merge of both.
 template <int D, int kBits>
 int launch_shared(const fa::DecodeParams& own, const fa::SharedParams& sp, void* o, float* lse,
                   cudaStream_t stream) {
@@ -680,10 +687,9 @@ int launch_shared(const fa::DecodeParams& own, const fa::SharedParams& sp, void*
       if (rc == FA_OK) rc = launch_split16<D, kBits>(maps, pre, true, stream);
     }
   } else {
-    rc = launch_split_rows<D, kBits>(maps, own, false, stream);
-    if (rc == FA_OK)
-      rc = sp.R <= 128 ? launch_shared_prefix<D, kBits, true>(maps, sp, stream)
-                       : launch_shared_prefix<D, kBits, false>(maps, sp, stream);
+    rc = sp.R <= 128 ? launch_shared_prefix<D, kBits, true>(maps, sp, stream)
+                     : launch_shared_prefix<D, kBits, false>(maps, sp, stream);
+    if (rc == FA_OK) rc = launch_split_rows<D, kBits>(maps, own, true, stream);
   }
   if (rc != FA_OK) return rc;
   // four warps per row where one per row leaves the GPU idle over many partials
@@ -813,7 +819,7 @@ bool shared_splits(int B, int Hq, int Hkv, int D, long long max_prefix, long lon
     return false;
   if (static_cast<long long>(B) * Hq > 0x7fffffffLL) return false;
   *own = num_splits > 0 ? num_splits : shared_own_splits(B, Hq, Hkv, max_own);
-  *prefix = shared_prefix_splits(D, B, Hq, Hkv, max_prefix, *own);
+  *prefix = shared_prefix_splits(D, B, Hq, Hkv, max_prefix, *own, max_own);
   return *own <= 65535;
 }
 

@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(512, 1)
     fa_shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v, const SharedParams p) {
   using C = SharedCfg<D, kBits, kStream>;
-  asm volatile("griddepcontrol.launch_dependents;");  // (the merge waits on the device)
+  // the kernel of the sequences' own keys may start on the SMs that this grid leaves free
+  asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // the swizzled tiles need 1024-byte aligned shared memory, and there is no room to align it here
   if ((smem_u32(smem_raw) & 1023u) != 0) {
@@ -226,7 +227,6 @@ __global__ void __launch_bounds__(512, 1)
   if (nt == 0) {
     for (int r = threadIdx.x; r < live; r += blockDim.x)
       p.lse_part[split * rows + out_row(r)] = -INFINITY;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // (as below)
     return;
   }
   const bool act1 = kStream ? nt > 1 : live > 128;  // S tile 1 has work
@@ -752,9 +752,6 @@ __global__ void __launch_bounds__(512, 1)
     if (out0 < live) {
       const int mine = out0 + (lane & (kOut - 1));
       const int orow = static_cast<int>(out_row(min(mine, live - 1)));
-      // Launched as a programmatic dependent of the kernel that reads the sequences' own keys: this grid
-      // does not end before that one, so whoever waits for this one waits for both.
-      asm volatile("griddepcontrol.wait;" ::: "memory");
       if (lane < kOut && mine < live) p.lse_part[split * rows + orow] = lse_row * 0.69314718055994531f;
       constexpr int kLanes = D / 4;  // lanes of a row
       const int d = 4 * (lane % kLanes);
