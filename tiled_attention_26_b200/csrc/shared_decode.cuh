@@ -26,8 +26,8 @@
 // What bounds it: neither memory nor the tensor core but the chain of one tile - its softmax, then its
 // P V and its next Q K^T, before which the next softmax cannot start (P lies over S).  With two
 // tiles of 128 x 128 scores at D = 128, 4.6 thousand cycles a pair, of which a softmax warp computes 3.2 (exponentials 1.7,
-// scaling and maximum 0.6) and the tensor core 2.05; 32768 keys x 64 sequences x 32 / 8 heads 54 us, 640 TFLOP/s
-// (B200).  Two things cost most on the way there: the unrolled code of all roles in the instruction
+// scaling and maximum 0.6) and the tensor core 2.05; 32768 keys x 64 sequences x 32 / 8 heads on 144 SMs
+// 54 us, 640 TFLOP/s (B200).  Two things cost most on the way there: the unrolled code of all roles in the instruction
 // caches, hence the rolled loops wherever registers allow, and operands of tcgen05.mma in vector registers,
 // hence the converged MMA warp.
 // A single accumulator with three buffers of S, which lets S run ahead of the softmax, is no faster: the
