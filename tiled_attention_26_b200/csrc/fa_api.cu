@@ -573,10 +573,12 @@ long long split_slots(long long G) { return (G > 8 ? 2 : 3) * kSms; }
 //   split 10 us + 1.0 T per block of 16 rows;  tcgen05 14 us + 1.45 T, twice that for a block of 256 rows
 // (131072 keys, T = 55: 16 rows 70 / 93 us, 32 rows 117 / 95 us; 4096 keys, 48 rows 23 / 25 us, 96 rows
 // 29 / 27 us).  At D = 64 a block of 16 costs half, a tcgen05 tile, bound by its softmax, the same.
+// More CTAs of the split kernel than half of what fits, beside those of the own keys, would take a second wave.
 bool shared_through_split(int D, long long R, int Hkv, long long max_keys) {
   const double T = static_cast<double>(Hkv) * ((max_keys + 127) / 128) / kSms;
   const double tile = R <= 128 ? 1.0 : 2.0 * ((R + 255) / 256);
-  return split_blocks(R) * T < (D == 128 ? 1.45 : 2.2) * tile * T + 4.0;
+  return Hkv * split_blocks(R) <= split_slots(R) / 2 &&
+         split_blocks(R) * T < (D == 128 ? 1.45 : 2.2) * tile * T + 4.0;
 }
 
 // Splits of the prefix: the count with the least estimate of tile times, the smaller of equals.  A split
@@ -603,18 +605,18 @@ int shared_prefix_splits(int D, int B, int Hq, int Hkv, long long max_keys, int 
     const double time = base * tiles * (R <= 128 ? 1.4 : 2.5) + 9.0 * kSms;
     sms -= std::min<long long>(kSms / 5, static_cast<long long>(kSms * own_time / (own_time + time) + 0.5));
   }
-  int best = 1;
-  double best_cost = -1.0;
-  for (int s = 1; s <= limit && s <= tiles; ++s) {
-    const double per = static_cast<double>((tiles + s - 1) / s);
-    const double cost = few ? per + s / 17.0
-                            : static_cast<double>((base * s + sms - 1) / sms) * (per + 3.0) + s / 25.0;
-    if (best_cost < 0.0 || cost < best_cost) {
+  // by tiles a split, fewest first; of the counts with the same tiles a split, the smallest
+  long long best = 1;
+  double best_cost = 1e30;
+  for (long long per = (tiles + limit - 1) / limit; per <= tiles && per < best_cost; ++per) {
+    const long long s = (tiles + per - 1) / per;
+    const double cost = few ? per + s / 17.0 : (base * s + sms - 1) / sms * (per + 3.0) + s / 25.0;
+    if (cost <= best_cost) {
       best = s;
       best_cost = cost;
     }
   }
-  return best;
+  return static_cast<int>(best);
 }
 
 // Splits of the sequences' own keys where the caller leaves the choice to the library: pieces of 512 keys
