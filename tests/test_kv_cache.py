@@ -363,6 +363,22 @@ def test_bad_indices_are_reported_and_skipped(built, what):
 
 
 @gpu
+def test_deterministic_mode_fills_new_buffers(built):
+    """Rows behind the last sequence of a buffer that the call allocates: NaN in deterministic mode."""
+    import torch
+    B, n, bt, pool, x, cu, dev = _paged_case(8, 2, 64, 16, [3, 0], [2, 1], 4)
+    args = (*dev["pool"], dev["bt"], n, dev["pos"], dev["cu"])
+    want = fa.fa_kv_gather_int8_paged(*args)
+    torch.use_deterministic_algorithms(True)
+    try:
+        got = fa.fa_kv_gather_int8_paged(*args)
+    finally:
+        torch.use_deterministic_algorithms(False)
+    for g, w in zip(got, want):
+        assert torch.equal(g[:3], w[:3]) and bool(g[3:].isnan().all())
+
+
+@gpu
 def test_zero_tokens(built):
     import torch
     B, n, bt, pool, x, cu, dev = _paged_case(8, 2, 64, 16, [3], [1], 0)

@@ -45,7 +45,7 @@ def build_calls(force: bool = False) -> str:
                 os.path.join(cuda, "include"), sysconfig.get_paths()["include"]):
         cmd += ["-isystem", inc]
     cmd += [CALLS_SOURCE, "-o", CALLS + ".tmp", "-L" + os.path.join(t, "lib"), "-ltorch", "-ltorch_cpu",
-            "-ltorch_python", "-lc10", "-lc10_cuda"]
+            "-ltorch_cuda", "-ltorch_python", "-lc10", "-lc10_cuda"]
     subprocess.run(cmd, check=True)
     os.replace(CALLS + ".tmp", CALLS)
     return CALLS

@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -62,10 +63,19 @@ bool optional(PyObject* o, at::ScalarType type, c10::Device dev, Shape shape, co
   return *out != nullptr && is(**out, type, dev, shape);
 }
 
+// A new tensor, without the dispatcher's way to it: a paged gather with its two outputs takes 5.3 us of
+// host time so, 5.9 us through at::empty. Deterministic mode fills new tensors, which at::empty does.
+at::Tensor empty(Shape shape, at::ScalarType type, c10::Device dev) {
+  const at::Context& ctx = at::globalContext();
+  if (ctx.deterministicAlgorithms() && ctx.deterministicFillUninitializedMemory())
+    return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  return at::detail::empty_cuda(shape, type, dev, c10::nullopt);
+}
+
 // An output argument: None -> a new tensor.
 bool output(PyObject* o, at::ScalarType type, c10::Device dev, Shape shape, at::Tensor* out) {
   if (o == Py_None) {
-    *out = at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+    *out = empty(shape, type, dev);
     return true;
   }
   const at::Tensor* t = tensor(o);
@@ -292,8 +302,7 @@ PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   if (a[14] == Py_None) {
     const size_t need = L.shared_bytes(p.B, static_cast<int>(Hq), p.Hkv, p.D, static_cast<int>(prefix_keys),
                                        static_cast<int>(own_keys), static_cast<int>(splits));
-    ws = at::empty({static_cast<int64_t>(std::max<size_t>(need, 1))},
-                   at::TensorOptions().dtype(at::kByte).device(dev));
+    ws = empty({static_cast<int64_t>(std::max<size_t>(need, 1))}, at::kByte, dev);
   } else {
     const at::Tensor* w = tensor(a[14]);
     if (w == nullptr || w->device() != dev || !w->is_contiguous()) return none();
@@ -302,7 +311,7 @@ PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   if (lse_in != nullptr)
     lse = *lse_in;
   else if (PyObject_IsTrue(a[15]) == 1)
-    lse = at::empty({B, Hq}, at::TensorOptions().dtype(at::kFloat).device(dev));
+    lse = empty({B, Hq}, at::kFloat, dev);
   float* lse_ptr = lse.defined() ? ptr_as<float>(lse) : nullptr;
   const int rc =
       bits == 8
