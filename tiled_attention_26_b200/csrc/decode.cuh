@@ -641,7 +641,7 @@ __device__ __forceinline__ void decode_split(const CUtensorMap& tm_k, const CUte
         for (int rr = 0; rr < 2; ++rr) {
           const int row = r_w + 16 * u + kslot(g + 8 * rr);
           vsc[u][rr] = (T + 16 * u + kslot(g + 8 * rr) < t_end) ? lds32f(vs_s + 4 * row) : 0.f;
-          vmax = fmaxf(vmax, vsc[u][rr]);
+          vmax = fmaxf(vmax, fabsf(vsc[u][rr]));
         }
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
