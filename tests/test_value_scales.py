@@ -1,5 +1,5 @@
-"""Decode over caches whose value scales span a wide range: negative scales (a value is code * scale, whatever
-the sign).  Against the definition in 64 bits.
+"""Decode over caches whose value scales span a wide range: blocks of zero rows (which the write stores with
+scale 0) and negative scales (a value is code * scale, whatever the sign).  Against the definition in 64 bits.
 
 Bound of the differences, per output element: the output to bf16 (half a step, 2^-8 of the value); the
 probabilities, the value scales and their products with the codes to fp16 (2^-11 each, of sum p |v|); fp16
@@ -80,6 +80,15 @@ def agree(o, lse, q, k, v, scale):
     assert (err <= 2.0 ** -15 * X + 2.0 ** -20 + 2.0 ** -21 * np.abs(L)).all(), err.max()
 
 
+def zero_rows(n, size):
+    """The first n rows hold zeros, the others values of magnitude ``size``."""
+    def change(c):
+        c.scales[1] *= np.float32(size)
+        c.scales[1][:, :n] = 0
+        c.codes[1][:, :n] = 0
+    return change
+
+
 def negative(c):
     """Small scales first, larger ones of the other sign behind them; keys' signs at random."""
     rng = np.random.default_rng(5)
@@ -93,7 +102,7 @@ def all_negative(c):
     c.scales[1] *= -1
 
 
-CHANGES = [negative, all_negative]
+CHANGES = [zero_rows(128, 1e-4), zero_rows(32, 2.0 ** -14), zero_rows(128, 1e3), negative, all_negative]
 
 
 @gpu
@@ -107,6 +116,14 @@ def test_decode(built, bits, D, S, splits, change):
     pool, table, lens = c.paged()
     c.check(*getattr(fa, name + "_paged")(q, *pool, table, lens, num_splits=splits))
     assert fa.fa_device_status() == 0
+
+
+def shared_zero(c):
+    """Zeros on the prefix's first 128 keys and on each sequence's first 64; small values elsewhere."""
+    c.scales[1] *= np.float32(1e-4)
+    for pg in [*c.pt[:128 // c.P], *c.bt[:, 0][[n > 0 for n in c.lens]]]:
+        c.scales[1][pg] = 0
+        c.codes[1][pg] = 0
 
 
 def shared_negative(c):
@@ -135,7 +152,7 @@ def shared_case(bits, B, Hq, Hkv, D, prefix, change):
 @gpu
 @pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("B,Hq,Hkv,D,prefix", SHARED)
-@pytest.mark.parametrize("change", [shared_negative])
+@pytest.mark.parametrize("change", [shared_zero, shared_negative])
 def test_shared_decode(built, bits, B, Hq, Hkv, D, prefix, change):
     c = shared_case(bits, B, Hq, Hkv, D, prefix, change)
     c.check(*c.call())

@@ -115,9 +115,10 @@ __device__ __forceinline__ float bf16_bits_to_float(uint16_t b) {
   return __uint_as_float(static_cast<uint32_t>(b) << 16);
 }
 
-// Power of two 2^e with e chosen so that x * 2^e < 2^top (x > 0), clamped to a safe range.
+// Power of two 2^e with e chosen so that x * 2^e < 2^top (x >= 0), clamped to a safe range.  Zero bounds
+// nothing and takes the largest e: a block of zeros must not lower the exponent of what follows it.
 __device__ __forceinline__ int pow2_exponent_below(float x, int top) {
-  if (!(x > 0.f)) return 0;
+  if (!(x > 0.f)) return 100;
   int ex;
   frexpf(x, &ex);  // x = f * 2^ex, f in [0.5, 1): x < 2^ex
   return max(-100, min(100, top - ex));
