@@ -1,5 +1,6 @@
 """Decode over caches whose value scales span a wide range: blocks of zero rows (which the write stores with
-scale 0) and negative scales (a value is code * scale, whatever the sign).  Against the definition in 64 bits.
+scale 0), negative scales (a value is code * scale, whatever the sign), and values and queries near the ends of
+bf16's range.  Against the definition in 64 bits.
 
 Bound of the differences, per output element: the output to bf16 (half a step, 2^-8 of the value); the
 probabilities, the value scales and their products with the codes to fp16 (2^-11 each, of sum p |v|); fp16
@@ -102,7 +103,22 @@ def all_negative(c):
     c.scales[1] *= -1
 
 
-CHANGES = [zero_rows(128, 1e-4), zero_rows(32, 2.0 ** -14), zero_rows(128, 1e3), negative, all_negative]
+def huge_values(c):
+    c.scales[1] *= np.float32(2.0 ** 122)
+
+
+def tiny_values(c):
+    c.scales[1] *= np.float32(2.0 ** -100)
+
+
+def huge_queries(c):
+    """Queries of 2^118 over keys of 2^-118: ordinary scores."""
+    c.scales[0] *= np.float32(2.0 ** -118)
+    c.qb = ((bf16_to_f64(c.qb) * 2.0 ** 118).astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+
+
+CHANGES = [zero_rows(128, 1e-4), zero_rows(32, 2.0 ** -14), zero_rows(128, 1e3), negative, all_negative,
+           huge_values, tiny_values, huge_queries]
 
 
 @gpu
@@ -152,7 +168,7 @@ def shared_case(bits, B, Hq, Hkv, D, prefix, change):
 @gpu
 @pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("B,Hq,Hkv,D,prefix", SHARED)
-@pytest.mark.parametrize("change", [shared_zero, shared_negative])
+@pytest.mark.parametrize("change", [shared_zero, shared_negative, huge_values, tiny_values, huge_queries])
 def test_shared_decode(built, bits, B, Hq, Hkv, D, prefix, change):
     c = shared_case(bits, B, Hq, Hkv, D, prefix, change)
     c.check(*c.call())

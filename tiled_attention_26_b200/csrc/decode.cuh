@@ -115,13 +115,14 @@ __device__ __forceinline__ float bf16_bits_to_float(uint16_t b) {
   return __uint_as_float(static_cast<uint32_t>(b) << 16);
 }
 
-// Power of two 2^e with e chosen so that x * 2^e < 2^top (x >= 0), clamped to a safe range.  Zero bounds
-// nothing and takes the largest e: a block of zeros must not lower the exponent of what follows it.
+// Power of two 2^e with e chosen so that x * 2^e < 2^top (x >= 0); every finite x has such an e for top >= 7, and
+// 2^e and 2^-e are normal numbers.  Zero bounds nothing and takes the largest e: a block of zeros must not lower
+// the exponent of what follows it.
 __device__ __forceinline__ int pow2_exponent_below(float x, int top) {
   if (!(x > 0.f)) return 100;
   int ex;
   frexpf(x, &ex);  // x = f * 2^ex, f in [0.5, 1): x < 2^ex
-  return max(-100, min(100, top - ex));
+  return max(-121, min(100, top - ex));
 }
 
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((127 + e) << 23); }
@@ -749,7 +750,11 @@ __device__ __forceinline__ void decode_split(const CUtensorMap& tm_k, const CUte
   float* sm_o = reinterpret_cast<float*>(smem + C::kMergeO);
   float* sm_m = reinterpret_cast<float*>(smem + C::kMergeM);
   float* sm_l = reinterpret_cast<float*>(smem + C::kMergeL);
-  const float unscale = (E == kEUnset) ? 0.f : exp2i_or_zero(-E);
+  // Until they are divided by the sum of the weights, sums of values near the end of the range would overflow:
+  // they are held in units of 2^24 (128 thousand keys of the largest weight, 2^8, or 2^25 of weight 1).  Results
+  // below 2^-102 lose bits of their fp32 there, below 2^-117 of bf16.
+  constexpr int kRoom = 24;
+  const float unscale = (E == kEUnset) ? 0.f : exp2i(-E - kRoom);
   // INT4: the odd dims (rows g + 8 of each m-tile) were accumulated from 16 x the codes
   const float unscale_hi = kBits == 4 ? unscale * 0.0625f : unscale;
 #pragma unroll
@@ -795,10 +800,11 @@ __device__ __forceinline__ void decode_split(const CUtensorMap& tm_k, const CUte
         acc.z += f * o.z;
         acc.w += f * o.w;
       }
+      const float Lr = L * exp2i(-kRoom);
       const size_t row = static_cast<size_t>(split) * p.rows + row_of(8 * z + h);
       *reinterpret_cast<float4*>(p.o_part + row * D + d) =
           (L == 0.f) ? make_float4(0.f, 0.f, 0.f, 0.f)
-                     : make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L);
+                     : make_float4(acc.x / Lr, acc.y / Lr, acc.z / Lr, acc.w / Lr);
       if (d == 0) p.lse_part[row] = (L == 0.f) ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
     }
   }
@@ -860,6 +866,8 @@ __global__ void __launch_bounds__(128) fa_decode_combine_kernel(const CombinePar
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  // (weighted by 2^-17 exp(L_s - M), which keeps a sum over 2^16 splits of values near the end of the range
+  // finite; undone with the division)
   // lane i weighs split s0 + kWarps i; a split with log-sum-exp -inf holds no key and is not read
   for (int s0 = w0; s0 < p.splits; s0 += 32 * kWarps) {
     const int own = s0 + kWarps * lane;
@@ -870,7 +878,7 @@ __global__ void __launch_bounds__(128) fa_decode_combine_kernel(const CombinePar
     const int n = min(32, (p.splits - s0 + kWarps - 1) / kWarps);
 #pragma unroll 8
     for (int s = 0; s < n; ++s) {
-      const float w = __shfl_sync(0xffffffffu, mine, s);
+      const float w = __shfl_sync(0xffffffffu, mine * 0x1p-17f, s);
       const bool read = some >> s & 1;
       const float* src = p.o_part + ((s0 + kWarps * s) * stride + row) * D + V * lane;
       if constexpr (V == 4) {
@@ -903,7 +911,7 @@ __global__ void __launch_bounds__(128) fa_decode_combine_kernel(const CombinePar
       for (int i = 0; i < V; ++i) acc[i] += sm_acc[w][V * lane + i];
     }
   }
-  const float inv = (L == 0.f) ? 0.f : 1.f / L;
+  const float inv = (L == 0.f) ? 0.f : 1.f / L * 0x1p17f;
   uint16_t* dst = p.o + static_cast<size_t>(row) * D + V * lane;
   if constexpr (V == 4) {
     uint2 w2;
