@@ -103,6 +103,14 @@ __device__ __forceinline__ long long shfl64(long long x, int from) {
   return static_cast<long long>(static_cast<unsigned long long>(hi) << 32 | lo);
 }
 
+// Of the `tokens` token rows from tok0 on, those that may be read: rows behind the last sequence need not exist.
+__host__ __device__ inline int kv_rows_to_read(const KvMap& m, long long tok0, int tokens) {
+  int end = m.N;
+  if (m.cu_tokens != nullptr && m.cu_tokens[m.B] < end) end = m.cu_tokens[m.B];
+  const long long left = end - tok0;
+  return left <= 0 ? 0 : left < tokens ? static_cast<int>(left) : tokens;
+}
+
 // The first block reports token offsets that do not start at 0, do not ascend, or pass N.
 __device__ __forceinline__ void kv_check_cu(const KvMap& m) {
   if (m.cu_tokens == nullptr || blockIdx.x != 0) return;
@@ -185,12 +193,12 @@ __global__ void __launch_bounds__(256) fa_kv_write_kernel(const KvCopyParams p) 
   const bool is_v = rest & 1;
   const long long tok0 = static_cast<long long>(rest >> 1) * kTokens;
   if constexpr (kPaged) kv_check_cu(map);
-  if (tok0 >= map.N) return;
+  const int left = kv_rows_to_read(map, tok0, kTokens);
+  if (left == 0) return;
   const long long stride = is_v ? p.v_stride : p.k_stride;
   const uint16_t* x = (is_v ? p.v : p.k) + tok0 * stride + static_cast<long long>(head) * D;
   uint8_t* codes = is_v ? p.v_codes : p.k_codes;
   float* scales = is_v ? p.v_scale : p.k_scale;
-  const int left = static_cast<int>(min(static_cast<long long>(kTokens), map.N - tok0));
 
   const int l = lane % kLanes;
   uint4 w[kU][2];
