@@ -14,7 +14,7 @@ LIB = os.path.join(HERE, "libfa.so")
 CALLS = os.path.join(HERE, "_torch_calls.so")
 CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
 SOURCES = [os.path.join(CSRC, "fa_api.cu")]
-DEPS = SOURCES + sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")) + [
+DEPS = SOURCES + sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))) + [
     os.path.join(ROOT, "include", "fa.h")]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
