@@ -87,3 +87,27 @@ def test_many_tiles_of_one_cta(built, plan, bits, D, rows, kind):
     assert kernel == ("streams" if rows == 20 else "blocks") and tiles >= 9
     c.check(*c.call())
     assert fa.fa_device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("which", ["ks", "vs"])
+@pytest.mark.parametrize("tile", [0, 1])
+@pytest.mark.parametrize("bits,D", [(8, 128), (8, 64), (4, 128)])
+def test_nan_of_a_stream_of_vanishing_weight(built, plan, bits, D, tile, which):
+    """Keys of one stream outweigh the other's by more than 2^126; a NaN scale in the light one still makes every row
+    that reads it NaN, and no other."""
+    import torch
+    c = long_case(bits, D, 20, seed=5)
+    kernel, tiles = plan_of(plan, c)
+    assert kernel == "streams" and tiles == 10
+    d = c.dev
+    pages = torch.from_numpy(np.ascontiguousarray(c.pt[:20])).cuda().long().view(10, 2)  # of each tile
+    d["ks"][pages[1 - tile::2].flatten()] *= 200
+    o, lse = c.call()
+    assert torch.isfinite(o).all()
+    d[which][int(pages[6 + tile, 1]), 3, 9] = float("nan")
+    o2, lse2 = c.call()
+    assert torch.isnan(o2[:, 0, 60:80]).all()
+    assert torch.isnan(lse2[:, 60:80]).all() if which == "ks" else torch.equal(lse2, lse)
+    o2[:, 0, 60:80] = o[:, 0, 60:80]
+    assert torch.equal(o2, o)

@@ -744,8 +744,9 @@ __global__ void __launch_bounds__(512, 1)
       const float sum = w0 + w1;
       lse_row = sum == 0.f ? -INFINITY : top + log2f(sum);
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      w0 *= inv;
-      w1 *= inv;
+      // -1: a stream without keys, which has staged nothing. A weight of 0 still counts: its stream may hold a NaN
+      w0 = a == -INFINITY ? -1.f : w0 * inv;
+      w1 = b == -INFINITY ? -1.f : w1 * inv;
     } else {
       __syncwarp();
     }
@@ -764,10 +765,9 @@ __global__ void __launch_bounds__(512, 1)
         if constexpr (kStream) {
           const float u0 = __shfl_sync(0xffffffffu, w0, w), u1 = __shfl_sync(0xffffffffu, w1, w);
           const uint4 z = lds128(piece(from + C::kTile, tile0 + w, d));
-          // (a stream without keys has staged nothing)
           auto merge = [&](uint32_t a, uint32_t b) {
-            return __float_as_uint((u0 == 0.f ? 0.f : u0 * __uint_as_float(a)) +
-                                   (u1 == 0.f ? 0.f : u1 * __uint_as_float(b)));
+            return __float_as_uint((u0 < 0.f ? 0.f : u0 * __uint_as_float(a)) +
+                                   (u1 < 0.f ? 0.f : u1 * __uint_as_float(b)));
           };
           y = make_uint4(merge(y.x, z.x), merge(y.y, z.y), merge(y.z, z.z), merge(y.w, z.w));
         }
