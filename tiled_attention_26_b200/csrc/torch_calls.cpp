@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/DimVector.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -63,6 +64,20 @@ bool optional(PyObject* o, at::ScalarType type, c10::Device dev, Shape shape, co
   return *out != nullptr && is(**out, type, dev, shape);
 }
 
+// Lets other Python threads run while a buffer is allocated and the kernels are launched: either may block (a
+// full launch queue, an allocator that waits for memory), and what it waits for may need Python.  What is
+// used meanwhile is held by the caller's frame; no Python object is touched.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 // A new tensor, without the dispatcher's way to it: a paged gather with its two outputs takes 5.3 us of
 // host time so, 5.9 us through at::empty. Deterministic mode fills new tensors, which at::empty does.
 at::Tensor empty(Shape shape, at::ScalarType type, c10::Device dev) {
@@ -72,15 +87,24 @@ at::Tensor empty(Shape shape, at::ScalarType type, c10::Device dev) {
   return at::detail::empty_cuda(shape, type, dev, c10::nullopt);
 }
 
-// An output argument: None -> a new tensor.
-bool output(PyObject* o, at::ScalarType type, c10::Device dev, Shape shape, at::Tensor* out) {
-  if (o == Py_None) {
-    *out = empty(shape, type, dev);
-    return true;
+// An output argument: the caller's tensor, or None, for which make() allocates one (without the interpreter's
+// lock, after every argument has been checked).
+struct Output {
+  at::Tensor t;
+  at::ScalarType type;
+  at::DimVector shape;
+
+  void make(c10::Device dev) {
+    if (!t.defined()) t = empty(shape, type, dev);
   }
+};
+bool output(PyObject* o, at::ScalarType type, c10::Device dev, Shape shape, Output* out) {
+  out->type = type;
+  out->shape = shape;
+  if (o == Py_None) return true;
   const at::Tensor* t = tensor(o);
   if (t == nullptr || !is(*t, type, dev, shape)) return false;
-  *out = *t;
+  out->t = *t;
   return true;
 }
 
@@ -171,16 +195,19 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
       (cu == nullptr && k->dim() == 4 && k->size(0) != p.B))
     return none();
   const int N = static_cast<int>(n);
-  const int rc =
-      bits == 8
-          ? L.append8(k->data_ptr(), v->data_ptr(), ks, vs, ptr_as<int8_t>(p.k), ptr_as<int8_t>(p.v),
-                      ptr_as<float>(p.ks), ptr_as<float>(p.vs), ptr_as<int32_t>(p.table),
-                      ptr_as<int32_t>(pos), ptr_as<int32_t>(cu), N, p.B, p.Hkv, p.page, p.max_pages,
-                      p.pages, p.D, stream_of(dev))
-          : L.append4(k->data_ptr(), v->data_ptr(), ks, vs, ptr_as<uint8_t>(p.k), ptr_as<uint8_t>(p.v),
-                      ptr_as<float>(p.ks), ptr_as<float>(p.vs), ptr_as<int32_t>(p.table),
-                      ptr_as<int32_t>(pos), ptr_as<int32_t>(cu), N, p.B, p.Hkv, p.page, p.max_pages,
-                      p.pages, p.D, stream_of(dev));
+  int rc;
+  {
+    Unlocked unlocked;
+    rc = bits == 8
+             ? L.append8(k->data_ptr(), v->data_ptr(), ks, vs, ptr_as<int8_t>(p.k), ptr_as<int8_t>(p.v),
+                         ptr_as<float>(p.ks), ptr_as<float>(p.vs), ptr_as<int32_t>(p.table),
+                         ptr_as<int32_t>(pos), ptr_as<int32_t>(cu), N, p.B, p.Hkv, p.page, p.max_pages,
+                         p.pages, p.D, stream_of(dev))
+             : L.append4(k->data_ptr(), v->data_ptr(), ks, vs, ptr_as<uint8_t>(p.k), ptr_as<uint8_t>(p.v),
+                         ptr_as<float>(p.ks), ptr_as<float>(p.vs), ptr_as<int32_t>(p.table),
+                         ptr_as<int32_t>(pos), ptr_as<int32_t>(cu), N, p.B, p.Hkv, p.page, p.max_pages,
+                         p.pages, p.D, stream_of(dev));
+  }
   return PyLong_FromLong(rc);
 }
 
@@ -195,22 +222,28 @@ PyObject* kv_gather(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   const at::Tensor *pos, *cu;
   if (overflow || !fits_int(n) || !pool(a + 1, a[5], bits, &p)) return none();
   const c10::Device dev = p.k->device();
-  at::Tensor k, v;
+  Output k, v;
   if (!optional(a[7], at::kInt, dev, {p.B}, &pos) || !optional(a[8], at::kInt, dev, {p.B + 1}, &cu) ||
       !output(a[9], at::kBFloat16, dev, {n, p.Hkv, p.D}, &k) ||
       !output(a[10], at::kBFloat16, dev, {n, p.Hkv, p.D}, &v))
     return none();
   const int N = static_cast<int>(n);
-  const int rc =
-      bits == 8
-          ? L.gather8(ptr_as<int8_t>(p.k), ptr_as<int8_t>(p.v), ptr_as<float>(p.ks), ptr_as<float>(p.vs),
-                      ptr_as<int32_t>(p.table), ptr_as<int32_t>(pos), ptr_as<int32_t>(cu), k.data_ptr(),
-                      v.data_ptr(), N, p.B, p.Hkv, p.page, p.max_pages, p.pages, p.D, stream_of(dev))
-          : L.gather4(ptr_as<uint8_t>(p.k), ptr_as<uint8_t>(p.v), ptr_as<float>(p.ks),
-                      ptr_as<float>(p.vs), ptr_as<int32_t>(p.table), ptr_as<int32_t>(pos),
-                      ptr_as<int32_t>(cu), k.data_ptr(), v.data_ptr(), N, p.B, p.Hkv, p.page,
-                      p.max_pages, p.pages, p.D, stream_of(dev));
-  return Py_BuildValue("(iNN)", rc, THPVariable_Wrap(k), THPVariable_Wrap(v));
+  int rc;
+  {
+    Unlocked unlocked;
+    k.make(dev);
+    v.make(dev);
+    rc = bits == 8
+             ? L.gather8(ptr_as<int8_t>(p.k), ptr_as<int8_t>(p.v), ptr_as<float>(p.ks),
+                         ptr_as<float>(p.vs), ptr_as<int32_t>(p.table), ptr_as<int32_t>(pos),
+                         ptr_as<int32_t>(cu), k.t.data_ptr(), v.t.data_ptr(), N, p.B, p.Hkv, p.page,
+                         p.max_pages, p.pages, p.D, stream_of(dev))
+             : L.gather4(ptr_as<uint8_t>(p.k), ptr_as<uint8_t>(p.v), ptr_as<float>(p.ks),
+                         ptr_as<float>(p.vs), ptr_as<int32_t>(p.table), ptr_as<int32_t>(pos),
+                         ptr_as<int32_t>(cu), k.t.data_ptr(), v.t.data_ptr(), N, p.B, p.Hkv, p.page,
+                         p.max_pages, p.pages, p.D, stream_of(dev));
+  }
+  return Py_BuildValue("(iNN)", rc, THPVariable_Wrap(k.t), THPVariable_Wrap(v.t));
 }
 
 // (bits, k, v, k_codes, v_codes, k_scale, v_scale) -> (status, k_codes, v_codes, k_scale, v_scale)
@@ -222,7 +255,7 @@ PyObject* kv_quantize(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   const c10::Device dev = k->device();
   const int64_t B = k->size(0), S = k->size(1), H = k->size(2), D = k->size(3);
   const int64_t row = bits == 8 ? D : D / 2;
-  at::Tensor kc, vc, ks, vs;
+  Output kc, vc, ks, vs;
   if (!fits_int(B) || !fits_int(S) || !fits_int(H) || !fits_int(D) ||
       !is(*k, at::kBFloat16, dev, {B, S, H, D}) || !is(*v, at::kBFloat16, dev, {B, S, H, D}) ||
       !output(a[3], code_type(bits), dev, {B, S, H, row}, &kc) ||
@@ -231,14 +264,18 @@ PyObject* kv_quantize(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     return none();
   const int b = static_cast<int>(B), s = static_cast<int>(S), h = static_cast<int>(H),
             d = static_cast<int>(D);
-  const int rc = bits == 8 ? L.quantize8(k->data_ptr(), v->data_ptr(), ptr_as<int8_t>(kc),
-                                         ptr_as<int8_t>(vc), ptr_as<float>(ks), ptr_as<float>(vs), b, s,
-                                         h, d, stream_of(dev))
-                           : L.quantize4(k->data_ptr(), v->data_ptr(), ptr_as<uint8_t>(kc),
-                                         ptr_as<uint8_t>(vc), ptr_as<float>(ks), ptr_as<float>(vs), b,
-                                         s, h, d, stream_of(dev));
-  return Py_BuildValue("(iNNNN)", rc, THPVariable_Wrap(kc), THPVariable_Wrap(vc), THPVariable_Wrap(ks),
-                       THPVariable_Wrap(vs));
+  int rc;
+  {
+    Unlocked unlocked;
+    for (Output* x : {&kc, &vc, &ks, &vs}) x->make(dev);
+    rc = bits == 8 ? L.quantize8(k->data_ptr(), v->data_ptr(), ptr_as<int8_t>(kc.t), ptr_as<int8_t>(vc.t),
+                                 ptr_as<float>(ks.t), ptr_as<float>(vs.t), b, s, h, d, stream_of(dev))
+                   : L.quantize4(k->data_ptr(), v->data_ptr(), ptr_as<uint8_t>(kc.t),
+                                 ptr_as<uint8_t>(vc.t), ptr_as<float>(ks.t), ptr_as<float>(vs.t), b, s, h,
+                                 d, stream_of(dev));
+  }
+  return Py_BuildValue("(iNNNN)", rc, THPVariable_Wrap(kc.t), THPVariable_Wrap(vc.t),
+                       THPVariable_Wrap(ks.t), THPVariable_Wrap(vs.t));
 }
 
 // (bits, k_codes, v_codes, k_scale, v_scale, k, v) -> (status, k, v)
@@ -250,7 +287,7 @@ PyObject* kv_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   const c10::Device dev = kc->device();
   const int64_t B = kc->size(0), S = kc->size(1), H = kc->size(2), row = kc->size(3);
   const int64_t D = bits == 8 ? row : 2 * row;
-  at::Tensor k, v;
+  Output k, v;
   if (!fits_int(B) || !fits_int(S) || !fits_int(H) || !fits_int(D) ||
       !is(*kc, code_type(bits), dev, {B, S, H, row}) || !is(*vc, code_type(bits), dev, {B, S, H, row}) ||
       !is(*ks, at::kFloat, dev, {B, H, S}) || !is(*vs, at::kFloat, dev, {B, H, S}) ||
@@ -259,13 +296,19 @@ PyObject* kv_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     return none();
   const int b = static_cast<int>(B), s = static_cast<int>(S), h = static_cast<int>(H),
             d = static_cast<int>(D);
-  const int rc = bits == 8 ? L.dequantize8(ptr_as<int8_t>(*kc), ptr_as<int8_t>(*vc), ptr_as<float>(*ks),
-                                           ptr_as<float>(*vs), k.data_ptr(), v.data_ptr(), b, s, h, d,
-                                           stream_of(dev))
-                           : L.dequantize4(ptr_as<uint8_t>(*kc), ptr_as<uint8_t>(*vc),
-                                           ptr_as<float>(*ks), ptr_as<float>(*vs), k.data_ptr(),
-                                           v.data_ptr(), b, s, h, d, stream_of(dev));
-  return Py_BuildValue("(iNN)", rc, THPVariable_Wrap(k), THPVariable_Wrap(v));
+  int rc;
+  {
+    Unlocked unlocked;
+    k.make(dev);
+    v.make(dev);
+    rc = bits == 8 ? L.dequantize8(ptr_as<int8_t>(*kc), ptr_as<int8_t>(*vc), ptr_as<float>(*ks),
+                                   ptr_as<float>(*vs), k.t.data_ptr(), v.t.data_ptr(), b, s, h, d,
+                                   stream_of(dev))
+                   : L.dequantize4(ptr_as<uint8_t>(*kc), ptr_as<uint8_t>(*vc), ptr_as<float>(*ks),
+                                   ptr_as<float>(*vs), k.t.data_ptr(), v.t.data_ptr(), b, s, h, d,
+                                   stream_of(dev));
+  }
+  return Py_BuildValue("(iNN)", rc, THPVariable_Wrap(k.t), THPVariable_Wrap(v.t));
 }
 
 // (bits, q, k_pages, v_pages, k_scale_pages, v_scale_pages, prefix_table, prefix_len, block_table,
@@ -297,36 +340,43 @@ PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   const int64_t prefix_keys = static_cast<int64_t>(max_prefix) * p.page;
   const int64_t own_keys = static_cast<int64_t>(p.max_pages) * p.page;
   if (overflow || !fits_int(splits) || !fits_int(prefix_keys) || !fits_int(own_keys)) return none();
-  at::Tensor o, ws, lse;
+  Output o;
+  at::Tensor ws, lse;
   if (!output(a[12], at::kBFloat16, dev, {B, 1, Hq, p.D}, &o)) return none();
-  if (a[14] == Py_None) {
-    const size_t need = L.shared_bytes(p.B, static_cast<int>(Hq), p.Hkv, p.D, static_cast<int>(prefix_keys),
-                                       static_cast<int>(own_keys), static_cast<int>(splits));
-    ws = empty({static_cast<int64_t>(std::max<size_t>(need, 1))}, at::kByte, dev);
-  } else {
+  if (a[14] != Py_None) {
     const at::Tensor* w = tensor(a[14]);
     if (w == nullptr || w->device() != dev || !w->is_contiguous()) return none();
     ws = *w;
   }
-  if (lse_in != nullptr)
-    lse = *lse_in;
-  else if (PyObject_IsTrue(a[15]) == 1)
-    lse = empty({B, Hq}, at::kFloat, dev);
-  float* lse_ptr = lse.defined() ? ptr_as<float>(lse) : nullptr;
-  const int rc =
-      bits == 8
-          ? L.shared8(q->data_ptr(), ptr_as<int8_t>(p.k), ptr_as<int8_t>(p.v), ptr_as<float>(p.ks),
-                      ptr_as<float>(p.vs), ptr_as<int32_t>(pt), ptr_as<int32_t>(pl),
-                      ptr_as<int32_t>(p.table), ptr_as<int32_t>(sl), o.data_ptr(), lse_ptr, p.B,
-                      static_cast<int>(Hq), p.Hkv, p.page, max_prefix, p.max_pages, p.pages, p.D,
-                      static_cast<float>(scale), static_cast<int>(splits), ws.data_ptr(), ws.nbytes(),
-                      stream_of(dev))
-          : L.shared4(q->data_ptr(), ptr_as<uint8_t>(p.k), ptr_as<uint8_t>(p.v), ptr_as<float>(p.ks),
-                      ptr_as<float>(p.vs), ptr_as<int32_t>(pt), ptr_as<int32_t>(pl),
-                      ptr_as<int32_t>(p.table), ptr_as<int32_t>(sl), o.data_ptr(), lse_ptr, p.B,
-                      static_cast<int>(Hq), p.Hkv, p.page, max_prefix, p.max_pages, p.pages, p.D,
-                      static_cast<float>(scale), static_cast<int>(splits), ws.data_ptr(), ws.nbytes(),
-                      stream_of(dev));
+  const int return_lse = PyObject_IsTrue(a[15]);
+  if (return_lse < 0) return none();
+  if (lse_in != nullptr) lse = *lse_in;
+  int rc;
+  {
+    Unlocked unlocked;
+    o.make(dev);
+    if (!ws.defined()) {
+      const size_t need =
+          L.shared_bytes(p.B, static_cast<int>(Hq), p.Hkv, p.D, static_cast<int>(prefix_keys),
+                         static_cast<int>(own_keys), static_cast<int>(splits));
+      ws = empty({static_cast<int64_t>(std::max<size_t>(need, 1))}, at::kByte, dev);
+    }
+    if (!lse.defined() && return_lse) lse = empty({B, Hq}, at::kFloat, dev);
+    float* lse_ptr = lse.defined() ? ptr_as<float>(lse) : nullptr;
+    rc = bits == 8
+             ? L.shared8(q->data_ptr(), ptr_as<int8_t>(p.k), ptr_as<int8_t>(p.v), ptr_as<float>(p.ks),
+                         ptr_as<float>(p.vs), ptr_as<int32_t>(pt), ptr_as<int32_t>(pl),
+                         ptr_as<int32_t>(p.table), ptr_as<int32_t>(sl), o.t.data_ptr(), lse_ptr, p.B,
+                         static_cast<int>(Hq), p.Hkv, p.page, max_prefix, p.max_pages, p.pages, p.D,
+                         static_cast<float>(scale), static_cast<int>(splits), ws.data_ptr(), ws.nbytes(),
+                         stream_of(dev))
+             : L.shared4(q->data_ptr(), ptr_as<uint8_t>(p.k), ptr_as<uint8_t>(p.v), ptr_as<float>(p.ks),
+                         ptr_as<float>(p.vs), ptr_as<int32_t>(pt), ptr_as<int32_t>(pl),
+                         ptr_as<int32_t>(p.table), ptr_as<int32_t>(sl), o.t.data_ptr(), lse_ptr, p.B,
+                         static_cast<int>(Hq), p.Hkv, p.page, max_prefix, p.max_pages, p.pages, p.D,
+                         static_cast<float>(scale), static_cast<int>(splits), ws.data_ptr(), ws.nbytes(),
+                         stream_of(dev));
+  }
   PyObject* lse_obj;
   if (lse.defined()) {
     lse_obj = THPVariable_Wrap(lse);
@@ -334,7 +384,7 @@ PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     Py_INCREF(Py_None);
     lse_obj = Py_None;
   }
-  return Py_BuildValue("(iNN)", rc, THPVariable_Wrap(o), lse_obj);
+  return Py_BuildValue("(iNN)", rc, THPVariable_Wrap(o.t), lse_obj);
 }
 
 // Nothing is launched when a C++ exception (an allocation that fails) ends F: the Python function then
