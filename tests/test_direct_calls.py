@@ -1,5 +1,5 @@
 """The direct calls for torch tensors (csrc/torch_calls.cpp): other Python threads run while one is inside the
-library."""
+library, and only a file built for the running torch and Python is loaded."""
 import ctypes
 import subprocess
 import threading
@@ -8,6 +8,7 @@ import time
 import pytest
 
 import tiled_attention_26_b200 as fa
+from tiled_attention_26_b200 import build
 from test_kv_cache import built  # noqa: F401
 
 gpu = pytest.mark.gpu
@@ -81,3 +82,38 @@ def test_other_threads_run_meanwhile(slow_library, name):
     assert slow_library.count() == before + 1 and end - start >= SECONDS
     # a thread that waits a millisecond at a time: about 200 turns, none while the lock is held
     assert sum(start < x < end for x in ticks) >= 10
+
+
+class Compiles(Exception):
+    pass
+
+
+@pytest.mark.parametrize("what", ["torch", "python"])
+def test_another_torch_or_python_is_another_file(built, monkeypatch, what):
+    """After a change of version the old file is neither loaded nor taken for up to date."""
+    import torch
+    fa._direct()
+    here = build.calls_path()
+    if what == "torch":
+        monkeypatch.setattr(torch, "__version__", "999.0.0")
+    else:
+        monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: ".cpython-999-x86_64-linux-gnu.so")
+    there = build.calls_path()
+    assert there != here and not build.os.path.exists(there)
+    commands = []
+
+    def run(cmd, **kw):
+        commands.append(cmd)
+        raise Compiles
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    with pytest.raises(Compiles):
+        build.build_calls()
+    assert commands[0][commands[0].index("-o") + 1] == there + ".tmp"
+    monkeypatch.setattr(fa, "_direct_calls", None)
+    with pytest.raises(RuntimeError, match="build.py"):
+        fa._direct()
+    monkeypatch.undo()
+    assert build.build_calls() == here
+    monkeypatch.setattr(fa, "_direct_calls", None)
+    assert fa._direct().kv_append is not None

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.util
 import math
 import os
 
@@ -114,13 +115,16 @@ def _direct():
     if _direct_calls is None:
         L = lib()
         import torch  # noqa: F401  (its libraries must be loaded first)
-        try:
-            from . import _torch_calls
-        except ImportError as e:
-            raise RuntimeError("_torch_calls.so is not built; run "
-                               "`python tiled_attention_26_b200/build.py`") from e
-        _torch_calls.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _CALLS))
-        _direct_calls = _torch_calls
+        from .build import calls_path
+        path = calls_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"the direct calls are not built for this torch and Python ({path}); run "
+                               "`python tiled_attention_26_b200/build.py`")
+        spec = importlib.util.spec_from_file_location(__name__ + "._torch_calls", path)
+        calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(calls)
+        calls.init(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _CALLS))
+        _direct_calls = calls
     return _direct_calls
 
 

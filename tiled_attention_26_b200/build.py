@@ -1,4 +1,4 @@
-"""Build ``libfa.so`` (the C-ABI attention library) for sm_100a with nvcc, and ``_torch_calls.so`` (its
+"""Build ``libfa.so`` (the C-ABI attention library) for sm_100a with nvcc, and ``_torch_calls.*.so`` (its
 direct calls for torch tensors) with the host compiler, in-tree."""
 from __future__ import annotations
 
@@ -11,7 +11,6 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfa.so")
-CALLS = os.path.join(HERE, "_torch_calls.so")
 CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
 SOURCES = [os.path.join(CSRC, "fa_api.cu")]
 DEPS = SOURCES + sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))) + [
@@ -33,9 +32,19 @@ def _stale(out: str, deps) -> bool:
     return not os.path.exists(out) or os.path.getmtime(out) < max(os.path.getmtime(p) for p in deps)
 
 
+def calls_path() -> str:
+    """File of the direct calls for the running torch and Python.  Their code holds the layouts of both, so
+    one built for another version is another file and is never loaded."""
+    import torch
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(HERE, f"_torch_calls.torch-{torch.__version__}-cxx11abi{abi}"
+                        f"{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_calls(force: bool = False) -> str:
-    if not force and not _stale(CALLS, [CALLS_SOURCE, os.path.join(ROOT, "include", "fa.h")]):
-        return CALLS
+    out = calls_path()
+    if not force and not _stale(out, [CALLS_SOURCE, os.path.join(ROOT, "include", "fa.h")]):
+        return out
     import torch
     t = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
@@ -44,11 +53,11 @@ def build_calls(force: bool = False) -> str:
     for inc in (os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
                 os.path.join(cuda, "include"), sysconfig.get_paths()["include"]):
         cmd += ["-isystem", inc]
-    cmd += [CALLS_SOURCE, "-o", CALLS + ".tmp", "-L" + os.path.join(t, "lib"), "-ltorch", "-ltorch_cpu",
+    cmd += [CALLS_SOURCE, "-o", out + ".tmp", "-L" + os.path.join(t, "lib"), "-ltorch", "-ltorch_cpu",
             "-ltorch_cuda", "-ltorch_python", "-lc10", "-lc10_cuda"]
     subprocess.run(cmd, check=True)
-    os.replace(CALLS + ".tmp", CALLS)
-    return CALLS
+    os.replace(out + ".tmp", out)
+    return out
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
