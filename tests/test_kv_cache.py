@@ -505,3 +505,40 @@ def test_refusals_on_the_gpu(built):
         fa.fa_kv_quantize_int8(odd, odd)
     for got, w in zip(dev["pool"], pool):
         assert np.array_equal(got.cpu().numpy(), w)
+
+
+@gpu
+@pytest.mark.parametrize("bits,Hkv,D,P", [(8, 2, 128, 16), (4, 3, 64, 16)])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_replayed_append_writes_the_right_rows(built, bits, Hkv, D, P, ragged):
+    """A captured append replayed while positions, inputs and token counts change in place: every code and scale of the
+    pool is what the appends in turn leave, the rows that no replay concerns included.  Ragged: num_tokens is
+    an upper bound, most of whose rows belong to no sequence."""
+    import torch
+    hist, most = [3, 10, 20], [5, 3, 9]
+    B, n, bt, pool, x, cu, dev = _paged_case(bits, Hkv, D, P, hist, most, 4)
+    steps = [[5, 0, 9], [1, 2, 0], [0, 0, 0], [2, 1, 3]] if ragged else [[2, 2, 2], [1, 1, 1]]
+    n = n if ragged else 6
+    src = [torch.zeros(n, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    starts = torch.tensor([0] * B, dtype=torch.int32, device="cuda")
+    call = lambda k: _call("append", bits, True)(  # noqa: E731
+        *(t[:k] for t in src), *dev["pool"], dev["bt"], starts, dev["cu"] if ragged else None)
+    graphs = {}
+    for i, new in enumerate(steps):
+        k = n if ragged else sum(new)
+        if k not in graphs:
+            graphs[k] = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graphs[k]):
+                call(k)
+        x = [make_rows(80 + 2 * i + w, (k, Hkv, D), "normal") for w in range(2)]
+        cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        for t, b in zip(src, x):
+            t[:k].copy_(_bf16(b))
+        dev["cu"].copy_(torch.from_numpy(cu))
+        starts.copy_(torch.tensor(hist, dtype=torch.int32))
+        graphs[k].replay()
+        pool, _ = _written(bits, P, hist, bt, pool, x, cu)
+        for got, w in zip(dev["pool"], pool):
+            assert np.array_equal(got.cpu().numpy(), w), i
+        hist = [h + t for h, t in zip(hist, new)]
+    assert fa.fa_device_status() == 0
