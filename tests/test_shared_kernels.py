@@ -69,6 +69,10 @@ def test_other_tests_reach_every_kernel(plan):
     assert kernels.count("streams") >= 5 and kernels.count("blocks") >= 5
 
 
+def test_the_smoke_run_reaches_the_tcgen05_kernel(plan):
+    assert plan(3, 2400, 60, 128, 256, 64)[0] == "streams"
+
+
 def long_case(bits, D, rows, kind="normal", seed=1):
     """75 KV heads: a CTA each, which takes the whole prefix of 10 tiles."""
     return Case(bits, 2, 75 * rows, 75, D, 64, 10 * 128 - 37, [70, 3], kind=kind, seed=seed)
