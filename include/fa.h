@@ -161,6 +161,8 @@ FA_API size_t fa_decode_int8_workspace_bytes(int B, int Hq, int D, int num_split
  *           bytes, owned by the caller; its contents on entry do not matter.  Two calls that may
  *           run concurrently must not share one workspace.
  * The query sees every key (causal alignment of a single query at the end of the sequence).
+ * Scales may have either sign and be 0.  Queries and values may have any finite size; scores are formed in
+ * fp32 from the query scaled to below 2^15, so keys of 2^105 and more can overflow to NaN.
  * D must be 64 or 128; Hq must be a multiple of Hkv.
  */
 FA_API int fa_decode_int8(const void* q, const int8_t* k, const int8_t* v, const float* k_scale,
@@ -376,7 +378,8 @@ FA_API int fa_kv_gather_int4_paged(const uint8_t* k_pages, const uint8_t* v_page
  *                 LSE = -inf.
  *   max_prefix_pages, max_pages_per_seq  times page_size at most 2^30 each.
  *   num_splits    splits of the own keys as for fa_decode_int8_paged, or 0: the library chooses (no
- *                 piece smaller than 512 keys).  How the prefix is split, and the kernel that reads it,
+ *                 piece smaller than 512 keys, and one piece where B * Hkv * ceil(Hq / Hkv / 16) > 444, or 296
+ *                 for more than 8 query heads per KV head: give 4 to 8 for own keys of thousands).  How the prefix is split, and the kernel that reads it,
  *                 follow from the sizes given here, not from prefix_len.
  *   workspace     at least fa_decode_shared_workspace_bytes(B, Hq, Hkv, D, max_prefix_pages *
  *                 page_size, max_pages_per_seq * page_size, num_splits) bytes, 16-byte aligned;

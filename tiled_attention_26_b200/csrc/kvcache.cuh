@@ -7,7 +7,8 @@
 // scale NaN and codes 0, so that whatever reads it is NaN rather than silently wrong.  The read
 // is bf16(fl32(code * scale)).  Both move every byte once and are bound by HBM: 268 M elements written to
 // INT8 in 130 us (6.3 TB/s, 0.96 of a copy's rate) and read back in 129; ragged tokens in pages reach 0.78
-// of it (33 K tokens of 8 heads, 40 + 36 us), INT4 rows of 64 dims, 14 instructions an element, 0.6.
+// of it (33 K tokens of 8 heads, 39 + 39 us), INT4 rows of 64 dims, 14 instructions an element, 0.6 (55 K tokens of
+// 5 heads, 22.5 + 25; 21.4 + 25 where the rows are loaded before the offset that says how many there are is read).
 //
 // Both kernels see the cache as pages of P tokens: codes [page][P][Hkv][row bytes], scales
 // [page][Hkv][P].  A contiguous cache [B, S, Hkv, ...] is the case P = S, page = sequence.
