@@ -104,3 +104,16 @@ def test_decode_pair_kernels_fit_as_the_single_ones(kernels):
         else:
             assert v["regs"] * 32 * 3 <= REGFILE // 4, (name, v)
         assert v["spill"] <= 32, (name, v)
+
+
+def test_merge_kernels_hold_a_batch_of_partial_rows(kernels):
+    # <D, warps a row, splits in flight>: 8 splits' rows of D / 32 values a lane do not fit 32 registers (a merge of many
+    # splits then takes twice as long); the others leave room for 12 and 16 CTAs an SM
+    found = _select(kernels, "_ZN2fa24fa_decode_combine_kernelI")
+    assert len(found) == 6, sorted(found)
+    for name, v in found.items():
+        if "ELi1ELi8EEE" in name:
+            assert v["regs"] >= (48 if "ILi128E" in name else 36), (name, v)
+        else:
+            assert v["regs"] * 128 * (12 if "ELi4ELi4EEE" in name else 16) <= REGFILE, (name, v)
+        assert v["spill"] == 0, (name, v)

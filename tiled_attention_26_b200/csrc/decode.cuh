@@ -848,8 +848,13 @@ __global__ void __launch_bounds__(160, kHB == 1 ? 3 : 2) fa_decode_pair_kernel(
 // lane merges D/32 output dims with vector loads, several splits in flight at once.  Launched as a
 // programmatic dependent of the split kernel: its CTAs may start while the split kernel drains and
 // wait at griddepcontrol.wait until every partial is written and visible.
-template <int D, int kWarps = 1>
-__global__ void __launch_bounds__(128) fa_decode_combine_kernel(const CombineParams p) {
+// kBatch splits of a warp are in flight at once.  Latency bounds it where rows are few: a call of 4 rows of 512 splits
+// takes 42 us with 8 in flight, 102 where each load stands beside its use (which the compiler returns to unless
+// few CTAs an SM are asked of it).  Where rows are many, CTAs hide the latency and registers cost them: 4 in flight
+// for four warps a row (2784 rows of 12 splits: 2 us slower with 8), 2 for one (32768 rows of 2 splits 117 us,
+// 123 with 8).
+template <int D, int kWarps, int kBatch>
+__global__ void __launch_bounds__(128, kBatch == 8 ? 4 : kBatch == 4 ? 12 : 16) fa_decode_combine_kernel(const CombineParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int V = D / 32;  // dims per lane
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -876,21 +881,32 @@ __global__ void __launch_bounds__(128) fa_decode_combine_kernel(const CombinePar
     L += mine;
     const uint32_t some = __ballot_sync(0xffffffffu, ls != -INFINITY);
     const int n = min(32, (p.splits - s0 + kWarps - 1) / kWarps);
-#pragma unroll 8
-    for (int s = 0; s < n; ++s) {
-      const float w = __shfl_sync(0xffffffffu, mine * 0x1p-17f, s);
-      const bool read = some >> s & 1;
-      const float* src = p.o_part + ((s0 + kWarps * s) * stride + row) * D + V * lane;
-      if constexpr (V == 4) {
-        const float4 x = read ? *reinterpret_cast<const float4*>(src) : make_float4(0, 0, 0, 0);
-        acc[0] += w * x.x;
-        acc[1 % V] += w * x.y;
-        acc[2 % V] += w * x.z;
-        acc[3 % V] += w * x.w;
-      } else {
-        const float2 x = read ? *reinterpret_cast<const float2*>(src) : make_float2(0, 0);
-        acc[0] += w * x.x;
-        acc[1 % V] += w * x.y;
+    // (loads without a branch: an empty split's reads split 0's row)
+#pragma unroll 1
+    for (int s = 0; s < n; s += kBatch) {
+      float x[kBatch][V];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const bool read = some >> (s + u) & 1;
+        const float* src = p.o_part + ((read ? s0 + kWarps * (s + u) : 0) * stride + row) * D + V * lane;
+        if constexpr (V == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(src);
+          x[u][0] = y.x;
+          x[u][1 % V] = y.y;
+          x[u][2 % V] = y.z;
+          x[u][3 % V] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(src);
+          x[u][0] = y.x;
+          x[u][1 % V] = y.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const float w = __shfl_sync(0xffffffffu, mine * 0x1p-17f, s + u);
+        const bool read = some >> (s + u) & 1;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += w * (read ? x[u][i] : 0.f);
       }
     }
   }

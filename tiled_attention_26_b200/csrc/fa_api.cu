@@ -413,7 +413,10 @@ int launch_combine(const fa::DecodeParams& p, int splits, void* o, float* lse, c
   cp.Hq = p.Hq;
   cp.splits = splits;
   const long long rows = static_cast<long long>(p.B) * p.Hq;
-  return launch(fa::fa_decode_combine_kernel<D, kWarps>,
+  // rows whose CTAs (4 rows each, 8 per SM) fit the GPU at once: 8 splits in flight; more: more CTAs per SM
+  return launch(kWarps == 4              ? fa::fa_decode_combine_kernel<D, 4, 4>
+                : rows <= 32 * fa::kSms ? fa::fa_decode_combine_kernel<D, 1, 8>
+                                        : fa::fa_decode_combine_kernel<D, 1, 2>,
                 dim3(static_cast<unsigned>((rows * kWarps + 3) / 4)), 128, 0, true, stream, cp);
 }
 
