@@ -27,8 +27,8 @@ inline bool shared_through_split(int D, long long R, int Hkv, long long max_keys
 }
 
 // Splits of the prefix: the count with the least estimate of tile times, the smaller of equals.  A split
-// costs the merge 0.057 us, 1/17 of the split kernel's tile or 1/25 of the tcgen05 kernel's (one KV head,
-// 8 rows, 32768 keys: 256 / 128 / 64 splits 23 / 16.5 / 14.5 us).  Through the split kernel as many as
+// costs the merge about 0.06 us, 1/17 of the split kernel's tile or 1/25 of the tcgen05 kernel's (one KV head,
+// 8 rows, 32768 keys as one paged sequence: 256 / 128 / 64 / 32 splits 19.4 / 12.7 / 11.6 / 12.2 us).  Through the split kernel as many as
 // its CTAs find room for beside those of the own keys.  Otherwise one CTA per SM runs a split of one (KV head,
 // row block) in about (tiles + 3) tile times (start-up and epilogue count for three), in as many
 // waves as the CTAs need on the SMs that it leaves to the own keys' kernel: their share of the work, a
